@@ -296,8 +296,9 @@ def _quantize(x):
     x = x.float()
     amax = x.abs().amax(1, keepdim=True)
     tiny = amax < 127 * LEAST
-    scale = torch.where(amax == 0, 1.0, torch.where(tiny, LEAST, amax / 127))
-    inverse = torch.where(amax == 0, 1.0, torch.where(tiny, 1 / LEAST, 127 / torch.where(tiny, 1.0, amax)))
+    top = torch.full_like(amax, 127.0)      # as a tensor: by a number, torch multiplies with a rounded reciprocal
+    scale = torch.where(amax == 0, 1.0, torch.where(tiny, LEAST, amax / top))
+    inverse = torch.where(amax == 0, 1.0, torch.where(tiny, 1 / LEAST, top / torch.where(tiny, 1.0, amax)))
     return (x.double() * inverse.double()).round().to(torch.int8), scale[:, 0]
 
 
