@@ -60,6 +60,7 @@ typedef enum {
 #define DG_DEVERR_BAD_MASKED_M  0x4  /* masked: masked_m[g] < 0 or > M_max (clamped)       */
 #define DG_DEVERR_MIXED_TILE    0x8  /* contiguous: a 128-row tile holds two experts       */
 #define DG_DEVERR_TIMEOUT       0x10 /* a pipeline wait exceeded its time limit; CTA quit   */
+#define DG_DEVERR_BAD_LOGIT     0x20 /* gate: a logit or bias is NaN or +infinity           */
 
 /*
  * Dense FP8 GEMM, NT layout (juejin.cn article §5 "常规稠密 GEMM"; the
@@ -225,6 +226,93 @@ int dg_moe_permute(const int32_t* topk_ids, int T, int topk, int num_experts, co
                    void* stream);
 int dg_moe_unpermute_combine(const void* d_perm, const int32_t* row_of, const float* weights, int T, int topk, int N,
                              void* out, void* stream);
+
+/*
+ * Routing of tokens to experts: the topk_ids of the permutations and the
+ * weights of dg_moe_unpermute_combine, from the router's logits.
+ *   logits : [T][num_experts], BF16 (logits_dtype 0) or FP32 (logits_dtype 1)
+ *   bias   : FP32 [num_experts] added to the scores for the choice only, or NULL
+ *   s = softmax(l) (score_func DG_SCORE_SOFTMAX) or sigmoid(l) (DG_SCORE_SIGMOID);
+ *   c = s + bias.
+ * With n_group > 1 the experts form n_group equal groups in index order; a
+ * group's score is its largest c (group_top 1) or the sum of its two largest
+ * (group_top 2; of one where only one can be chosen), and the topk_group best
+ * groups stay.  Among their experts the topk with the largest c are chosen,
+ * best first, ties (of experts and of groups) to the lowest index.  The order is
+ * that of c in 64 bits; without a bias it is that of the logits.
+ *   topk_ids     : int32 [T][topk]
+ *   topk_weights : FP32 [T][topk], scale * s_j, or scale * s_j / sum_i s_i over the
+ *                  chosen experts (renormalize 1), however small the scores are.
+ * An expert with logit or bias -infinity is never chosen; slots left over hold id
+ * -1 and weight 0 (a padded token: every logit -infinity), which the permutations
+ * and the combine take as not routed.  A row with a NaN or +infinity (or such a
+ * bias) is not routed at all and sets DG_DEVERR_BAD_LOGIT.  At most 1024 experts,
+ * 32 groups and topk 32; topk <= topk_group * num_experts / n_group.
+ *
+ * dg_moe_gate_backward: d_logits [T][num_experts], in the logits' type, from
+ * d_weights FP32 [T][topk], the gradient of topk_weights, with the choice of
+ * experts held (it has no gradient; the bias takes part in nothing else).  Slots
+ * with id -1 are left out; a row without any other gets zeros.  An expert that is
+ * named twice in a row gets both gradients.  Ids outside [-1, num_experts) set
+ * DG_DEVERR_BAD_EXPERT and count as -1.  Every row of d_logits is written in full.
+ * Equal inputs give equal bits.  d_logits must not overlap logits.
+ */
+#define DG_SCORE_SOFTMAX 0
+#define DG_SCORE_SIGMOID 1
+int dg_moe_gate(const void* logits, int logits_dtype, const float* bias, int T, int num_experts, int topk,
+                int score_func, int n_group, int topk_group, int group_top, int renormalize, float scale,
+                int32_t* topk_ids, float* topk_weights, void* stream);
+int dg_moe_gate_backward(const void* logits, int logits_dtype, const int32_t* topk_ids, const float* d_weights, int T,
+                         int num_experts, int topk, int score_func, int renormalize, float scale, void* d_logits,
+                         void* stream);
+
+/*
+ * Int8 products with one scale per token and per output channel ("W8A8"),
+ * beside the block-scaled FP8 ones:
+ *   D[m][n] = sa[m] * sb[n] * sum_k A[m][k] * B[n][k]
+ * The products are summed exactly in int32; then FP32(sum) * sa * sb, each step
+ * rounded to FP32, is rounded to d's type.
+ *   a  : int8 [M][K]        sa : FP32 [M]
+ *   b  : int8 [N][K]        sb : FP32 [N]
+ *   d  : BF16 [M][N] (d_is_fp32 0) or FP32 [M][N] (d_is_fp32 1)
+ * K % 16 == 0, 0 < K <= 131056 (so that no sum leaves int32); N % 16 == 0; every
+ * pointer 16-byte aligned.  Layouts, streams and errors are those of the FP8
+ * entry points; the grouped forms take
+ *   contiguous : a [M_total][K], sa [M_total], b [G][N][K], sb [G][N], d BF16 [M_total][N],
+ *                m_indices as dg_m_grouped_fp8_gemm_nt_contiguous (and its device errors)
+ *   masked     : a [G][M_max][K], sa [G][M_max], b [G][N][K], sb [G][N], d BF16 [G][M_max][N],
+ *                masked_m as dg_m_grouped_fp8_gemm_nt_masked (and its device errors)
+ * and leave padding and masked rows of d as they were.
+ */
+int dg_int8_gemm_nt(const void* a, const float* sa, const void* b, const float* sb, void* d, int M, int N, int K,
+                    int d_is_fp32, void* stream);
+int dg_m_grouped_int8_gemm_nt_contiguous(const void* a, const float* sa, const void* b, const float* sb, void* d,
+                                         const int32_t* m_indices, int M_total, int N, int K, int num_groups,
+                                         void* stream);
+int dg_m_grouped_int8_gemm_nt_masked(const void* a, const float* sa, const void* b, const float* sb, void* d,
+                                     const int32_t* masked_m, int num_groups, int M_max, int N, int K, void* stream);
+
+/*
+ * Per-token int8 quantisation: the a / sa operands of the int8 products.
+ *   x     : [M][K] activations, BF16 (x_dtype 0) or FP32 (x_dtype 1), K % 16 == 0
+ *   q     : int8 [M][K]      scale : FP32 [M]
+ * For every row, with amax = max|x|: scale = fp32(amax / 127) and q = the integer
+ * nearest to x * fp32(127 / amax), ties to even (the product is not rounded first).
+ * A row of zeros has scale 1; one with amax < 127 * 2^-126 scale 2^-126 (x * 2^126).
+ * A row that holds a NaN or an infinity has scale NaN and codes 0.
+ *
+ * dg_moe_quantize_permute_int8: the same for routed tokens x [T][K], written
+ * straight into the contiguous layout of dg_moe_permute, whose rules for topk_ids,
+ * segments, M_cap, m_indices, row_of and src_of hold:
+ *   a_perm : int8 [M_cap][K]     sa_perm : FP32 [M_cap]
+ * Codes of padding and tail rows are not written, their scales are 0.  a_perm,
+ * sa_perm and m_indices feed dg_m_grouped_int8_gemm_nt_contiguous with M_total =
+ * M_cap.  With T = 0, topk_ids, x and row_of may be NULL.
+ */
+int dg_quantize_int8_per_token(const void* x, int x_dtype, void* q, float* scale, int M, int K, void* stream);
+int dg_moe_quantize_permute_int8(const int32_t* topk_ids, int T, int topk, int num_experts, const void* x, int x_dtype,
+                                 int K, void* a_perm, float* sa_perm, int32_t* m_indices, int32_t* row_of,
+                                 int32_t* src_of, int M_cap, void* stream);
 
 /* M alignment of expert segments in the contiguous layout (128). */
 int dg_get_mk_alignment_for_contiguous_layout(void);

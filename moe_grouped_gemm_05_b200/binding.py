@@ -30,6 +30,9 @@ DG_DEVERR_BAD_EXPERT = 0x2
 DG_DEVERR_BAD_MASKED_M = 0x4
 DG_DEVERR_MIXED_TILE = 0x8
 DG_DEVERR_TIMEOUT = 0x10
+DG_DEVERR_BAD_LOGIT = 0x20
+
+_SCORES = {"softmax": 0, "sigmoid": 1}
 
 _lib = None
 
@@ -63,6 +66,14 @@ def load() -> ctypes.CDLL:
     lib.dg_moe_permute_capacity.argtypes = [i, i, i]
     lib.dg_moe_permute.argtypes = [i32p, i, i, i, vp, i32p, i, vp, i32p, i32p, i32p, i32p, i, vp]
     lib.dg_moe_unpermute_combine.argtypes = [vp, i32p, vp, i, i, i, vp, vp]
+    f = ctypes.c_float
+    lib.dg_moe_gate.argtypes = [vp, i, vp, i, i, i, i, i, i, i, i, f, vp, vp, vp]
+    lib.dg_moe_gate_backward.argtypes = [vp, i, vp, vp, i, i, i, i, i, f, vp, vp]
+    lib.dg_int8_gemm_nt.argtypes = [vp, vp, vp, vp, vp, i, i, i, i, vp]
+    lib.dg_m_grouped_int8_gemm_nt_contiguous.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, vp]
+    lib.dg_m_grouped_int8_gemm_nt_masked.argtypes = [vp, vp, vp, vp, vp, vp, i, i, i, i, vp]
+    lib.dg_quantize_int8_per_token.argtypes = [vp, i, vp, vp, i, i, vp]
+    lib.dg_moe_quantize_permute_int8.argtypes = [vp, i, i, i, vp, i, i, vp, vp, vp, vp, vp, i, vp]
     lib.dg_packed_sf_words.argtypes = [i, i]
     lib.dg_packed_sf_words.restype = ctypes.c_int64
     lib.dg_get_mk_alignment_for_contiguous_layout.argtypes = []
@@ -79,7 +90,9 @@ def load() -> ctypes.CDLL:
     for name in ("dg_fp8_gemm_nt", "dg_m_grouped_fp8_gemm_nt_contiguous", "dg_m_grouped_fp8_gemm_nt_masked",
                  "dg_pack_sf_ue8m0", "dg_get_device_error", "dg_set_config", "dg_describe_config",
                  "dg_quantize_fp8_1x128", "dg_fp8_gemm_nt_ex", "dg_moe_permute_capacity", "dg_moe_permute",
-                 "dg_moe_unpermute_combine"):
+                 "dg_moe_unpermute_combine", "dg_moe_gate", "dg_moe_gate_backward", "dg_int8_gemm_nt",
+                 "dg_m_grouped_int8_gemm_nt_contiguous", "dg_m_grouped_int8_gemm_nt_masked",
+                 "dg_quantize_int8_per_token", "dg_moe_quantize_permute_int8"):
         getattr(lib, name).restype = ctypes.c_int
     _lib = lib
     return lib
@@ -387,6 +400,203 @@ def moe_unpermute_combine(d_perm: torch.Tensor, row_of: torch.Tensor, weights=No
     _check(load().dg_moe_unpermute_combine(_ptr(d_perm), _ptr(row_of), _ptr(weights) if weights is not None else None,
                                            T, topk, N, _ptr(out), _stream()))
     return out
+
+
+def _launch_stream(t: torch.Tensor) -> int:
+    """The current stream of t's device, which must be the current device: the library launches there."""
+    dev = t.get_device()
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"operands are on {t.device} but the current device is cuda:{torch.cuda.current_device()}")
+    return torch.cuda.current_stream(dev).cuda_stream
+
+
+def _operand(t, dtypes, shape, name: str, device) -> int:
+    """Checks one operand (dtype, shape, contiguity, device) and returns its address."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if t.shape != shape or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}, got shape "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+_FLOAT_CODES = {torch.bfloat16: 0, torch.float32: 1}
+_INT8, _I32T, _F32T, _BF16T = (torch.int8,), (torch.int32,), (torch.float32,), (torch.bfloat16,)
+_BF16_F32 = (torch.bfloat16, torch.float32)
+
+
+def _cuda_matrix(t, dtypes, name: str, dims: int = 2):
+    """Checks the leading operand of a call: its dtype, rank, and that it is a contiguous CUDA tensor."""
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
+    if not t.is_cuda or not t.is_contiguous() or t.dim() != dims:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dims} dimensions")
+
+
+def moe_gate(logits, topk: int, bias=None, *, score: str = "softmax", n_group: int = 1, topk_group: int = 1,
+             group_top: int = 1, renormalize: bool = False, scale: float = 1.0, ids=None, weights=None):
+    """Routes tokens to experts: (topk_ids int32 [T, topk], topk_weights float32 [T, topk]) from logits [T, E].
+
+    score: "softmax" or "sigmoid"; bias (float32 [E]) is added to the scores for the choice only.  With
+    n_group > 1 only the topk_group best groups stay, by their best expert (group_top=1) or the sum of their
+    two best (2).  The weights are scale * score, with renormalize divided by the sum over the chosen ones.
+    Experts with logit (or bias) -inf are never chosen; slots left over hold id -1 and weight 0.  The results
+    are the topk_ids of the permutations and the weights of moe_unpermute_combine.
+    """
+    if score not in _SCORES:
+        raise ValueError(f"unknown score {score!r}: softmax or sigmoid")
+    _cuda_matrix(logits, _BF16_F32, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    if ids is None:
+        ids = torch.empty((T, max(0, topk)), dtype=torch.int32, device=dev)
+    if weights is None:
+        weights = torch.empty((T, max(0, topk)), dtype=torch.float32, device=dev)
+    _check(load().dg_moe_gate(logits.data_ptr(), _FLOAT_CODES[logits.dtype],
+                              _operand(bias, _F32T, (E,), "bias", dev) if bias is not None else None, T, E, topk,
+                              _SCORES[score], n_group, topk_group, group_top, 1 if renormalize else 0, scale,
+                              _operand(ids, _I32T, (T, topk), "ids", dev),
+                              _operand(weights, _F32T, (T, topk), "weights", dev), _launch_stream(logits)))
+    return ids, weights
+
+
+def moe_gate_backward(logits, topk_ids, d_weights, *, score: str = "softmax", renormalize: bool = False,
+                      scale: float = 1.0, d_logits=None) -> torch.Tensor:
+    """Gradient of moe_gate's weights with respect to the logits, with the choice of experts (topk_ids) held.
+
+    d_weights: float32 [T, topk]; score, renormalize and scale as in the forward call.  Returns d_logits in the
+    logits' type: zero outside the chosen experts, except for softmax weights that are not renormalised.
+    """
+    if score not in _SCORES:
+        raise ValueError(f"unknown score {score!r}: softmax or sigmoid")
+    _cuda_matrix(logits, _BF16_F32, "logits")
+    _cuda_matrix(topk_ids, _I32T, "topk_ids")
+    T, E = logits.shape
+    topk = topk_ids.shape[1]
+    dev = logits.device
+    if d_logits is None:
+        d_logits = torch.empty_like(logits)
+    _check(load().dg_moe_gate_backward(logits.data_ptr(), _FLOAT_CODES[logits.dtype],
+                                       _operand(topk_ids, _I32T, (T, topk), "topk_ids", dev),
+                                       _operand(d_weights, _F32T, (T, topk), "d_weights", dev), T, E, topk,
+                                       _SCORES[score], 1 if renormalize else 0, scale,
+                                       _operand(d_logits, (logits.dtype,), (T, E), "d_logits", dev),
+                                       _launch_stream(logits)))
+    return d_logits
+
+
+def quantize_int8_per_token(x, q=None, scale=None):
+    """Per-token int8 quantisation of x[..., K] (bf16 or fp32): (q int8 [..., K], scale float32 [...]).
+
+    With x [M, K] (or [G, M_max, K]) these are the `a` / `sa` operands of the int8 products.
+    """
+    _cuda_matrix(x, _BF16_F32, "x", max(1, x.dim()))
+    lead, K = x.shape[:-1], x.shape[-1]
+    dev = x.device
+    if q is None:
+        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+    if scale is None:
+        scale = torch.empty(lead, dtype=torch.float32, device=dev)
+    qp, sp = _operand(q, _INT8, x.shape, "q", dev), _operand(scale, _F32T, lead, "scale", dev)
+    _check(load().dg_quantize_int8_per_token(x.data_ptr(), _FLOAT_CODES[x.dtype], qp, sp, lead.numel(), K,
+                                             _launch_stream(x)))
+    return q, scale
+
+
+def moe_quantize_permute_int8(topk_ids, num_experts: int, x, out=None):
+    """Per-token int8 quantisation of routed tokens x [T, K], written into the contiguous expert layout.
+
+    Returns a dict with a (int8 [M_cap, K]), sa (float32 [M_cap]), m_indices, src_of ([M_cap]) and row_of
+    ([T, topk]); a / sa / m_indices are the operands of m_grouped_int8_gemm_nt_contiguous.  `out`, if given, is
+    such a dict of preallocated tensors (M_cap = dg_moe_permute_capacity).
+    """
+    _cuda_matrix(topk_ids, _I32T, "topk_ids")
+    _cuda_matrix(x, _BF16_F32, "x")
+    T, topk = topk_ids.shape
+    K = x.shape[1]
+    if x.shape[0] != T:
+        raise ValueError(f"x must be [T, K] with T = {T} rows, one per token of topk_ids")
+    _same_device(x, topk_ids)
+    lib = load()
+    cap = lib.dg_moe_permute_capacity(T, topk, num_experts)
+    if cap < 0:
+        _check(cap)
+    dev = x.device
+    if out is None:
+        out = {
+            "a": torch.empty((cap, K), dtype=torch.int8, device=dev),
+            "sa": torch.empty((cap,), dtype=torch.float32, device=dev),
+            "m_indices": torch.empty((cap,), dtype=torch.int32, device=dev),
+            "src_of": torch.empty((cap,), dtype=torch.int32, device=dev),
+            "row_of": torch.empty((T, topk), dtype=torch.int32, device=dev),
+        }
+    else:
+        for key in ("a", "sa", "m_indices", "src_of", "row_of"):
+            if key not in out:
+                raise ValueError(f"out[{key!r}] is missing")
+    _check(lib.dg_moe_quantize_permute_int8(
+        topk_ids.data_ptr(), T, topk, num_experts, x.data_ptr(), _FLOAT_CODES[x.dtype], K,
+        _operand(out["a"], _INT8, (cap, K), "out['a']", dev), _operand(out["sa"], _F32T, (cap,), "out['sa']", dev),
+        _operand(out["m_indices"], _I32T, (cap,), "out['m_indices']", dev),
+        _operand(out["row_of"], _I32T, (T, topk), "out['row_of']", dev),
+        _operand(out["src_of"], _I32T, (cap,), "out['src_of']", dev), cap, _launch_stream(x)))
+    return out
+
+
+def int8_gemm_nt(a, sa, b, sb, d=None, out_dtype=torch.bfloat16) -> torch.Tensor:
+    """D[M,N] = sa[m] * sb[n] * (A[M,K] . B[N,K]^T), int8 operands, exact int32 sums.
+
+    sa: float32 [M], one scale per token; sb: float32 [N], one per output channel.  D is bf16, or float32 with
+    out_dtype=torch.float32 (or a float32 d).
+    """
+    _cuda_matrix(a, _INT8, "a")
+    M, K = a.shape
+    N = b.shape[0]
+    dev = a.device
+    if d is None:
+        if out_dtype not in _BF16_F32:
+            raise ValueError("out_dtype must be bfloat16 or float32")
+        d = torch.empty((M, N), dtype=out_dtype, device=dev)
+    _check(load().dg_int8_gemm_nt(a.data_ptr(), _operand(sa, _F32T, (M,), "sa", dev),
+                                  _operand(b, _INT8, (N, K), "b", dev), _operand(sb, _F32T, (N,), "sb", dev),
+                                  _operand(d, _BF16_F32, (M, N), "d", dev), M, N, K,
+                                  1 if d.dtype == torch.float32 else 0, _launch_stream(a)))
+    return d
+
+
+def m_grouped_int8_gemm_nt_contiguous(a, sa, b, sb, m_indices, d=None) -> torch.Tensor:
+    """Contiguous-layout grouped int8 GEMM: D[m] = sa[m] * sb[g] * (A[m] . B[g]^T), g = m_indices[m]; -1 rows
+    untouched.  a int8 [M_total, K], sa float32 [M_total], b int8 [G, N, K], sb float32 [G, N], D bf16."""
+    _cuda_matrix(a, _INT8, "a")
+    _cuda_matrix(b, _INT8, "b", 3)
+    M, K = a.shape
+    G, N, _ = b.shape
+    dev = a.device
+    if d is None:
+        d = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    _check(load().dg_m_grouped_int8_gemm_nt_contiguous(
+        a.data_ptr(), _operand(sa, _F32T, (M,), "sa", dev), _operand(b, _INT8, (G, N, K), "b", dev),
+        _operand(sb, _F32T, (G, N), "sb", dev), _operand(d, _BF16T, (M, N), "d", dev),
+        _operand(m_indices, _I32T, (M,), "m_indices", dev), M, N, K, G, _launch_stream(a)))
+    return d
+
+
+def m_grouped_int8_gemm_nt_masked(a, sa, b, sb, masked_m, d=None) -> torch.Tensor:
+    """Masked-layout grouped int8 GEMM: rows m < masked_m[g] of expert g; other rows untouched.
+
+    a int8 [G, M_max, K], sa float32 [G, M_max], b int8 [G, N, K], sb float32 [G, N], D bf16 [G, M_max, N]."""
+    _cuda_matrix(a, _INT8, "a", 3)
+    _cuda_matrix(b, _INT8, "b", 3)
+    G, M_max, K = a.shape
+    N = b.shape[1]
+    dev = a.device
+    if d is None:
+        d = torch.empty((G, M_max, N), dtype=torch.bfloat16, device=dev)
+    _check(load().dg_m_grouped_int8_gemm_nt_masked(
+        a.data_ptr(), _operand(sa, _F32T, (G, M_max), "sa", dev), _operand(b, _INT8, (G, N, K), "b", dev),
+        _operand(sb, _F32T, (G, N), "sb", dev), _operand(d, _BF16T, (G, M_max, N), "d", dev),
+        _operand(masked_m, _I32T, (G,), "masked_m", dev), G, M_max, N, K, _launch_stream(a)))
+    return d
 
 
 def get_device_error() -> int:

@@ -19,6 +19,9 @@
 #include "fp8_gemm_kernel.cuh"
 #include "quant_kernel.cuh"
 #include "moe_kernels.cuh"
+#include "gate_kernels.cuh"
+#include "int8_gemm_kernel.cuh"
+#include "int8_quant_kernel.cuh"
 
 namespace dg {
 
@@ -621,6 +624,214 @@ static int grid_size(int sms, long long tiles, const Config* cfg) {
   return static_cast<int>(units * cfg->ctas);
 }
 
+// ------------------------------------------------------------------ int8 configurations
+
+using Int8KernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Int8Args);
+
+// Host-side id of the dense int8 kernels with FP32 output.
+constexpr int MODE_INT8_DENSE_F32 = 3;
+
+template <int BN, int STAGES, int MODE, int CTAS, bool OUT_F32>
+static Config make_int8_config() {
+  Config c;
+  c.bn = BN;
+  c.stages = STAGES;
+  c.ctas = CTAS;
+  c.smem = Int8Layout<BN, STAGES, MODE, CTAS>::kSmemBytes;
+  c.num_acc = 2;
+  c.threads = kInt8Threads;
+  c.fn = reinterpret_cast<KernelFn>(&int8_gemm_kernel<BN, STAGES, MODE, CTAS, OUT_F32>);
+  return c;
+}
+
+// MODE: a mode of the kernel, or MODE_INT8_DENSE_F32.
+template <int MODE>
+static const Config* int8_config_table(int* count) {
+  constexpr bool f32 = MODE == MODE_INT8_DENSE_F32;
+  constexpr int mode = f32 ? MODE_DENSE : MODE;
+  static const Config table[] = {
+      make_int8_config<64, 8, mode, 1, f32>(), make_int8_config<128, 6, mode, 1, f32>(),
+      make_int8_config<256, 4, mode, 1, f32>(), make_int8_config<128, 8, mode, 2, f32>(),
+      make_int8_config<256, 6, mode, 2, f32>(),
+  };
+  *count = static_cast<int>(sizeof(table) / sizeof(table[0]));
+  return table;
+}
+
+// Time of one 128-wide K block of a tile and of the rest of a tile, in ns, as
+// in the FP8 kernels' cost model.
+static const CostParams kCostInt8[] = {
+    {64, 1, 1, false, 200, 600},  {128, 1, 1, false, 210, 750},   {256, 1, 1, false, 330, 1300},
+    {128, 2, 1, false, 220, 900}, {256, 2, 1, false, 310, 1500},
+};
+
+template <int MODE>
+static const Config* choose_int8_config(long long rows_est, int N, int K, int sms, int groups) {
+  constexpr int mode = MODE == MODE_INT8_DENSE_F32 ? MODE_DENSE : MODE;
+  int n = 0;
+  const Config* t = int8_config_table<MODE>(&n);
+  const auto pairs_fit = [&](const Config& c) {
+    return !(mode == MODE_CONTIG && c.ctas == 2 && rows_est / 128 > kMaxContigBlocks);
+  };
+  if (t_force_bn)
+    for (int i = 0; i < n; ++i)
+      if (t[i].bn == t_force_bn && (t_force_ctas == 0 || t[i].ctas == t_force_ctas) && t_force_pipes <= 1 &&
+          pairs_fit(t[i]))
+        return &t[i];
+  const Config* best = nullptr;
+  double best_cost = 1e300;
+  for (int i = 0; i < n; ++i) {
+    const Config& c = t[i];
+    if (!pairs_fit(c)) continue;
+    const CostParams& k = kCostInt8[i];
+    const long long tile_m = 128LL * c.ctas;
+    long long m_tiles;
+    if (mode == MODE_MASKED) {
+      const long long per = std::max<long long>(1, rows_est / std::max(1, groups));
+      m_tiles = static_cast<long long>(groups) * ((per + tile_m - 1) / tile_m);
+    } else {
+      m_tiles = (rows_est + tile_m - 1) / tile_m;
+      if (mode == MODE_CONTIG && c.ctas == 2) m_tiles += (groups + 1) / 2;
+    }
+    const long long n_tiles = (N + c.bn - 1) / c.bn;
+    const long long units = std::max(1, sms / c.ctas);
+    const double waves = static_cast<double>((m_tiles * n_tiles + units - 1) / units);
+    const double compute = waves * (((K + 127) / 128) * k.kb_ns + k.tile_ns);
+    const double bytes = static_cast<double>(rows_est) * (K + 2.0 * N) +
+                         (mode == MODE_DENSE ? 1.0 : groups) * static_cast<double>(N) * K;
+    const double memory = bytes / kHbmBytesPerNs;
+    const double cost = std::max(compute, memory) + 0.1 * std::min(compute, memory);
+    if (cost < best_cost * 0.999) {
+      best_cost = cost;
+      best = &c;
+    }
+  }
+  return best;
+}
+
+template <int MODE>
+static int launch_int8(const Config* cfg, int grid, const CUtensorMap* maps, Int8Args args, cudaStream_t stream) {
+  args.wait_limit_ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  constexpr int kMaxDevices = 64, kMaxConfigs = 8;
+  static std::mutex mu;
+  static bool attr_done[kMaxDevices][kMaxConfigs] = {};
+  int n = 0;
+  const int idx = static_cast<int>(cfg - int8_config_table<MODE>(&n));
+  int dev = 0;
+  DG_CUDA_TRY(cudaGetDevice(&dev));
+  if (idx < 0 || idx >= n || idx >= kMaxConfigs || dev < 0 || dev >= kMaxDevices)
+    return fail(DG_ERR_UNSUPPORTED, "configuration %d / device %d outside the launch table", idx, dev);
+  {
+    std::lock_guard<std::mutex> lock(mu);
+    if (!attr_done[dev][idx]) {
+      DG_CUDA_TRY(cudaFuncSetAttribute(reinterpret_cast<const void*>(cfg->fn),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, cfg->smem));
+      attr_done[dev][idx] = true;
+    }
+  }
+  DG_CUDA_TRY(launch_plain_smem(reinterpret_cast<Int8KernelFn>(cfg->fn), grid, cfg->threads,
+                                static_cast<size_t>(cfg->smem), stream, cfg->ctas, maps[0], maps[1], maps[2], args));
+  return DG_OK;
+}
+
+// One int8 call: rows of A per group, groups of A / D and of B.
+template <int MODE>
+static int int8_gemm(const void* a, const float* sa, const void* b, const float* sb, void* d, int rows, int GA, int N,
+                     int K, int GB, long long rows_est, const int32_t* m_indices, const int32_t* masked_m,
+                     cudaStream_t stream) {
+  constexpr bool f32 = MODE == MODE_INT8_DENSE_F32;
+  DeviceInfo di;
+  int r = device_info(&di);
+  if (r) return r;
+  const Config* cfg = choose_int8_config<MODE>(rows_est, N, K, usable_sms(di.sms), GB);
+  if (!cfg) return fail(DG_ERR_UNSUPPORTED, "no built configuration");
+  CUtensorMap maps[3];
+  if ((r = build_maps_cached(maps, cfg, a, b, d, rows, GA, N, K, GB, rows, GA, f32))) return r;
+  Int8Args args = {};
+  args.rows = rows;
+  args.N = N;
+  args.K = K;
+  args.G = GB;
+  args.num_m_blocks = (rows + 128 * cfg->ctas - 1) / (128 * cfg->ctas);
+  args.num_n_blocks = (N + cfg->bn - 1) / cfg->bn;
+  args.raster_m = raster_group(args.num_m_blocks);
+  args.m_indices = m_indices;
+  args.masked_m = masked_m;
+  if (f32) args.d32 = static_cast<float*>(d);
+  else args.d = static_cast<__nv_bfloat16*>(d);
+  args.sa = sa;
+  args.sb = sb;
+  const long long tiles = static_cast<long long>(GA) * args.num_m_blocks * args.num_n_blocks;
+  if (tiles > 0x7FFFFFFFLL) return fail(DG_ERR_SHAPE, "too many output tiles");
+  return launch_int8<MODE>(cfg, grid_size(di.sms, tiles, cfg), maps, args, stream);
+}
+
+// The largest K whose sum of products of two int8 values, 128 * 128 at most, stays below 2^31.
+constexpr int kInt8MaxK = 131056;
+
+// rows == 0 (nothing to do) passes with any pointers: an empty tensor has none.
+static int check_int8(const void* a, const float* sa, const void* b, const float* sb, const void* d, int rows, int N,
+                      int K) {
+  if (K <= 0 || K % 16 != 0 || K > kInt8MaxK)
+    return fail(DG_ERR_SHAPE, "K=%d must be a positive multiple of 16, at most %d", K, kInt8MaxK);
+  if (N <= 0 || N % 16 != 0) return fail(DG_ERR_SHAPE, "N=%d must be a positive multiple of 16", N);
+  if (rows < 0) return fail(DG_ERR_SHAPE, "%d rows of a: must be >= 0", rows);
+  if (rows == 0) return DG_OK;
+  if (!a || !sa || !b || !sb || !d) return fail(DG_ERR_NULL, "a, sa, b, sb and d must be non-NULL");
+  if (!aligned16(a) || !aligned16(b) || !aligned16(d) || !aligned16(sa) || !aligned16(sb))
+    return fail(DG_ERR_ALIGN, "a, sa, b, sb and d must be 16-byte aligned");
+  return DG_OK;
+}
+
+// ------------------------------------------------------------------ launches of the row kernels
+
+// quantize_int8_kernel over rows of K elements.  Units of 16 elements: one a
+// thread up to 512 threads, then two (and four in BF16, 32 registers) a thread
+// of up to 1024; a longer row is read twice.  Rows of one warp share a block of four.
+template <typename T, bool PERM>
+static cudaError_t launch_quantize_int8(const QuantArgs& p, cudaStream_t st) {
+  const int units = p.K / 16;
+  const int u = units <= 512 ? 1 : units <= 2048 ? 2 : (sizeof(T) == 2 && units <= 4096) ? 4 : 0;
+  const int warps = u == 0 ? 32 : (units + 32 * u - 1) / (32 * u);
+  const int teams = warps == 1 ? 4 : 1;
+  auto fn = u == 1   ? &quantize_int8_kernel<T, 1, PERM>
+            : u == 2 ? &quantize_int8_kernel<T, 2, PERM>
+            : u == 4 ? &quantize_int8_kernel<T, sizeof(T) == 2 ? 4 : 0, PERM>
+                     : &quantize_int8_kernel<T, 0, PERM>;
+  LaunchAttrs la(1);
+  cudaLaunchConfig_t lc = {};
+  lc.gridDim = dim3((p.M + teams - 1) / teams);
+  lc.blockDim = dim3(32, warps, teams);
+  lc.stream = st;
+  lc.attrs = la.attr;
+  lc.numAttrs = la.n;
+  return cudaLaunchKernelEx(&lc, fn, p);
+}
+
+// Elements a lane of the gate kernels holds: the smallest power of two that covers E.
+template <typename T>
+static cudaError_t launch_gate(const GateArgs& p, cudaStream_t st) {
+  const long long blocks = (static_cast<long long>(p.T) + kGateWarps - 1) / kGateWarps;
+  constexpr int th = 32 * kGateWarps;
+  if (p.E <= 32) return launch_plain(moe_gate_kernel<T, 1>, blocks, th, st, p);
+  if (p.E <= 64) return launch_plain(moe_gate_kernel<T, 2>, blocks, th, st, p);
+  if (p.E <= 128) return launch_plain(moe_gate_kernel<T, 4>, blocks, th, st, p);
+  if (p.E <= 256) return launch_plain(moe_gate_kernel<T, 8>, blocks, th, st, p);
+  if (p.E <= 512) return launch_plain(moe_gate_kernel<T, 16>, blocks, th, st, p);
+  return launch_plain(moe_gate_kernel<T, 32>, blocks, th, st, p);
+}
+template <typename T>
+static cudaError_t launch_gate_backward(const GateBackwardArgs& p, cudaStream_t st) {
+  const long long blocks = (static_cast<long long>(p.T) + kGateWarps - 1) / kGateWarps;
+  constexpr int th = 32 * kGateWarps;
+  if (p.E <= 32) return launch_plain(moe_gate_backward_kernel<T, 1>, blocks, th, st, p);
+  if (p.E <= 64) return launch_plain(moe_gate_backward_kernel<T, 2>, blocks, th, st, p);
+  if (p.E <= 128) return launch_plain(moe_gate_backward_kernel<T, 4>, blocks, th, st, p);
+  if (p.E <= 256) return launch_plain(moe_gate_backward_kernel<T, 8>, blocks, th, st, p);
+  if (p.E <= 512) return launch_plain(moe_gate_backward_kernel<T, 16>, blocks, th, st, p);
+  return launch_plain(moe_gate_backward_kernel<T, 32>, blocks, th, st, p);
+}
+
 // ------------------------------------------------------------------ pack kernel
 
 __global__ void pack_sf_ue8m0_kernel(const float* __restrict__ sf, uint32_t* __restrict__ out,
@@ -662,6 +873,29 @@ __global__ void take_error_kernel() { g_dg_error_taken = atomicExch(&g_dg_error,
 using namespace dg;
 
 // ==================================================================== C ABI
+
+// The routing kernel: one cluster; its table needs more than 48 KB of shared
+// memory beyond 320 experts.  scales: kp words a row, zeroed in padding rows.
+static int launch_route(const int32_t* topk_ids, int n, int num_experts, int M_cap, int kp, int32_t* m_indices,
+                        int32_t* row_of, int32_t* src_of, uint32_t* scales, cudaStream_t st) {
+  {
+    static std::mutex mu;
+    static bool attr_done[64] = {};
+    int dev = 0;
+    DG_CUDA_TRY(cudaGetDevice(&dev));
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev < 0 || dev >= 64) return fail(DG_ERR_UNSUPPORTED, "device %d outside the launch table", dev);
+    if (!attr_done[dev]) {
+      DG_CUDA_TRY(cudaFuncSetAttribute(reinterpret_cast<const void*>(&moe_route_kernel),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, route_smem_bytes(kMoeMaxExperts)));
+      attr_done[dev] = true;
+    }
+  }
+  DG_CUDA_TRY(launch_plain_smem(moe_route_kernel, kRouteCluster, kMoeThreads,
+                                static_cast<size_t>(route_smem_bytes(num_experts)), st, kRouteCluster, topk_ids, n,
+                                num_experts, M_cap, kp, m_indices, row_of, src_of, scales));
+  return DG_OK;
+}
 
 template <int HMODE>
 static int gemm_dense(const void* a, const void* sfa, const void* b, const int32_t* sfb, void* d, int M,
@@ -860,24 +1094,9 @@ int dg_moe_permute(const int32_t* topk_ids, int T, int topk, int num_experts, co
   if (r) return r;
   auto st = static_cast<cudaStream_t>(stream);
   const int kp = (K / 128 + 3) / 4;
-  // the routing kernel: one cluster; its table needs more than 48 KB of shared memory beyond 320 experts
-  {
-    static std::mutex mu;
-    static bool attr_done[64] = {};
-    int dev = 0;
-    DG_CUDA_TRY(cudaGetDevice(&dev));
-    std::lock_guard<std::mutex> lock(mu);
-    if (dev < 0 || dev >= 64) return fail(DG_ERR_UNSUPPORTED, "device %d outside the launch table", dev);
-    if (!attr_done[dev]) {
-      DG_CUDA_TRY(cudaFuncSetAttribute(reinterpret_cast<const void*>(&moe_route_kernel),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, route_smem_bytes(kMoeMaxExperts)));
-      attr_done[dev] = true;
-    }
-  }
-  DG_CUDA_TRY(launch_plain_smem(moe_route_kernel, kRouteCluster, kMoeThreads,
-                                static_cast<size_t>(route_smem_bytes(num_experts)), st, kRouteCluster, topk_ids,
-                                static_cast<int>(n), num_experts, M_cap, kp, m_indices, row_of, src_of,
-                                reinterpret_cast<uint32_t*>(sfa_perm)));
+  if ((r = launch_route(topk_ids, static_cast<int>(n), num_experts, M_cap, kp, m_indices, row_of, src_of,
+                        reinterpret_cast<uint32_t*>(sfa_perm), st)))
+    return r;
   const long long work = static_cast<long long>(T) * (K / 16);
   if (work == 0) return DG_OK;
   const long long blocks =
@@ -1062,6 +1281,192 @@ int dg_m_grouped_fp8_gemm_nt_masked_fp32sfa(const void* a, const float* sfa, con
                                             const int32_t* sfb, void* d, const int32_t* masked_m,
                                             int num_groups, int M_max, int N, int K, void* stream) {
   return masked_impl(a, sfa, b, sfb, d, masked_m, num_groups, M_max, N, K, stream, true);
+}
+
+int dg_int8_gemm_nt(const void* a, const float* sa, const void* b, const float* sb, void* d, int M, int N, int K,
+                    int d_is_fp32, void* stream) {
+  int r = check_int8(a, sa, b, sb, d, M, N, K);
+  if (r) return r;
+  if (d_is_fp32 != 0 && d_is_fp32 != 1) return fail(DG_ERR_UNSUPPORTED, "d_is_fp32=%d must be 0 or 1", d_is_fp32);
+  if (M == 0) return DG_OK;
+  auto st = static_cast<cudaStream_t>(stream);
+  if (d_is_fp32) return int8_gemm<MODE_INT8_DENSE_F32>(a, sa, b, sb, d, M, 1, N, K, 1, M, nullptr, nullptr, st);
+  return int8_gemm<MODE_DENSE>(a, sa, b, sb, d, M, 1, N, K, 1, M, nullptr, nullptr, st);
+}
+
+int dg_m_grouped_int8_gemm_nt_contiguous(const void* a, const float* sa, const void* b, const float* sb, void* d,
+                                         const int32_t* m_indices, int M_total, int N, int K, int num_groups,
+                                         void* stream) {
+  int r = check_int8(a, sa, b, sb, d, M_total, N, K);
+  if (r) return r;
+  if (num_groups <= 0) return fail(DG_ERR_SHAPE, "num_groups=%d must be positive", num_groups);
+  if (M_total % 128 != 0) return fail(DG_ERR_SHAPE, "M_total=%d must be a multiple of %d", M_total, 128);
+  if (M_total == 0) return DG_OK;
+  if (!m_indices) return fail(DG_ERR_NULL, "m_indices must be non-NULL");
+  return int8_gemm<MODE_CONTIG>(a, sa, b, sb, d, M_total, 1, N, K, num_groups, M_total, m_indices, nullptr,
+                                static_cast<cudaStream_t>(stream));
+}
+
+int dg_m_grouped_int8_gemm_nt_masked(const void* a, const float* sa, const void* b, const float* sb, void* d,
+                                     const int32_t* masked_m, int num_groups, int M_max, int N, int K, void* stream) {
+  int r = check_int8(a, sa, b, sb, d, M_max, N, K);
+  if (r) return r;
+  if (num_groups <= 0 || num_groups > kMaxMaskedGroups)
+    return fail(DG_ERR_SHAPE, "num_groups=%d must be in [1, %d]", num_groups, kMaxMaskedGroups);
+  if (M_max == 0) return DG_OK;
+  if (!masked_m) return fail(DG_ERR_NULL, "masked_m must be non-NULL");
+  // the device decides the real tile count; the heuristic assumes half-full experts
+  const long long rows_est = std::max<long long>(1, static_cast<long long>(num_groups) * M_max / 2);
+  return int8_gemm<MODE_MASKED>(a, sa, b, sb, d, M_max, num_groups, N, K, num_groups, rows_est, nullptr, masked_m,
+                                static_cast<cudaStream_t>(stream));
+}
+
+int dg_quantize_int8_per_token(const void* x, int x_dtype, void* q, float* scale, int M, int K, void* stream) {
+  if (x_dtype != 0 && x_dtype != 1) return fail(DG_ERR_UNSUPPORTED, "x_dtype=%d (0: bf16, 1: fp32)", x_dtype);
+  if (K <= 0 || K % 16 != 0) return fail(DG_ERR_SHAPE, "K=%d must be a positive multiple of 16", K);
+  if (M < 0) return fail(DG_ERR_SHAPE, "M=%d must be >= 0", M);
+  if (M == 0) return DG_OK;
+  if (!x || !q || !scale) return fail(DG_ERR_NULL, "x, q and scale must be non-NULL");
+  if (!aligned16(x) || !aligned16(q)) return fail(DG_ERR_ALIGN, "x and q must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(scale) & 3) != 0) return fail(DG_ERR_ALIGN, "scale must be 4-byte aligned");
+  DeviceInfo di;
+  int r = device_info(&di);
+  if (r) return r;
+  QuantArgs p = {};
+  p.x = x;
+  p.M = M;
+  p.K = K;
+  p.q = static_cast<uint8_t*>(q);
+  p.scale = scale;
+  auto st = static_cast<cudaStream_t>(stream);
+  if (x_dtype == 0) DG_CUDA_TRY((launch_quantize_int8<__nv_bfloat16, false>(p, st)));
+  else DG_CUDA_TRY((launch_quantize_int8<float, false>(p, st)));
+  return DG_OK;
+}
+
+int dg_moe_quantize_permute_int8(const int32_t* topk_ids, int T, int topk, int num_experts, const void* x, int x_dtype,
+                                 int K, void* a_perm, float* sa_perm, int32_t* m_indices, int32_t* row_of,
+                                 int32_t* src_of, int M_cap, void* stream) {
+  if (!a_perm || !sa_perm || !m_indices || !src_of || (T != 0 && (!topk_ids || !x || !row_of)))
+    return fail(DG_ERR_NULL, "every pointer must be non-NULL (topk_ids, x and row_of may be NULL when T = 0)");
+  if (x_dtype != 0 && x_dtype != 1) return fail(DG_ERR_UNSUPPORTED, "x_dtype=%d (0: bf16, 1: fp32)", x_dtype);
+  if (!aligned16(x) || !aligned16(a_perm) || !aligned16(sa_perm))
+    return fail(DG_ERR_ALIGN, "x, a_perm and sa_perm must be 16-byte aligned");
+  if (T < 0 || topk <= 0 || num_experts <= 0 || num_experts > kMoeMaxExperts)
+    return fail(DG_ERR_SHAPE, "T=%d topk=%d num_experts=%d (at most %d experts)", T, topk, num_experts, kMoeMaxExperts);
+  if (K <= 0 || K % 16 != 0) return fail(DG_ERR_SHAPE, "K=%d must be a positive multiple of 16", K);
+  const int cap = dg_moe_permute_capacity(T, topk, num_experts);
+  if (cap < 0) return cap;
+  if (M_cap < cap || M_cap % 128 != 0)
+    return fail(DG_ERR_SHAPE, "M_cap=%d must be a multiple of 128 and >= %d (dg_moe_permute_capacity)", M_cap, cap);
+  DeviceInfo di;
+  int r = device_info(&di);
+  if (r) return r;
+  auto st = static_cast<cudaStream_t>(stream);
+  // the scales are words of one K group: zero bits are the scale 0 of padding rows
+  if ((r = launch_route(topk_ids, T * topk, num_experts, M_cap, 1, m_indices, row_of, src_of,
+                        reinterpret_cast<uint32_t*>(sa_perm), st)))
+    return r;
+  if (T == 0) return DG_OK;
+  QuantArgs p = {};
+  p.x = x;
+  p.M = T;
+  p.K = K;
+  p.q = static_cast<uint8_t*>(a_perm);
+  p.scale = sa_perm;
+  p.ids = topk_ids;
+  p.row_of = row_of;
+  p.topk = topk;
+  p.m_indices = m_indices;
+  p.src_of = src_of;
+  if (x_dtype == 0) DG_CUDA_TRY((launch_quantize_int8<__nv_bfloat16, true>(p, st)));
+  else DG_CUDA_TRY((launch_quantize_int8<float, true>(p, st)));
+  return DG_OK;
+}
+
+static int check_gate(const void* logits, int logits_dtype, const void* ids, const void* w, const void* d, int T, int E,
+                      int topk, int score_func, int renormalize) {
+  if (logits_dtype != 0 && logits_dtype != 1)
+    return fail(DG_ERR_UNSUPPORTED, "logits_dtype=%d (0: bf16, 1: fp32)", logits_dtype);
+  if (score_func != DG_SCORE_SOFTMAX && score_func != DG_SCORE_SIGMOID)
+    return fail(DG_ERR_UNSUPPORTED, "score_func=%d (0: softmax, 1: sigmoid)", score_func);
+  if (renormalize != 0 && renormalize != 1) return fail(DG_ERR_UNSUPPORTED, "renormalize=%d must be 0 or 1", renormalize);
+  if (T < 0 || E <= 0 || E > kMoeMaxExperts)
+    return fail(DG_ERR_SHAPE, "T=%d num_experts=%d (1 to %d experts)", T, E, kMoeMaxExperts);
+  if (topk <= 0 || topk > kGateMaxTopk || topk > E)
+    return fail(DG_ERR_SHAPE, "topk=%d must be in [1, min(%d, num_experts=%d)]", topk, kGateMaxTopk, E);
+  if (T == 0) return DG_OK;
+  if (!logits || !ids || !w || !d) return fail(DG_ERR_NULL, "every pointer but bias must be non-NULL");
+  if (!aligned16(logits) || !aligned16(d)) return fail(DG_ERR_ALIGN, "logits and d_logits must be 16-byte aligned");
+  if ((reinterpret_cast<uintptr_t>(ids) & 3) != 0 || (reinterpret_cast<uintptr_t>(w) & 3) != 0)
+    return fail(DG_ERR_ALIGN, "topk_ids and the weights must be 4-byte aligned");
+  return DG_OK;
+}
+
+int dg_moe_gate(const void* logits, int logits_dtype, const float* bias, int T, int num_experts, int topk,
+                int score_func, int n_group, int topk_group, int group_top, int renormalize, float scale,
+                int32_t* topk_ids, float* topk_weights, void* stream) {
+  int r = check_gate(logits, logits_dtype, topk_ids, topk_weights, logits, T, num_experts, topk, score_func, renormalize);
+  if (r) return r;
+  if (bias && !aligned16(bias)) return fail(DG_ERR_ALIGN, "bias must be 16-byte aligned");
+  if (n_group <= 0 || n_group > kGateMaxGroups || num_experts % n_group != 0)
+    return fail(DG_ERR_SHAPE, "n_group=%d must divide num_experts=%d and be at most %d", n_group, num_experts,
+                kGateMaxGroups);
+  const int gsize = num_experts / n_group;
+  if (topk_group <= 0 || topk_group > n_group || topk > topk_group * gsize)
+    return fail(DG_ERR_SHAPE, "topk_group=%d must be in [1, n_group=%d] and leave topk=%d experts", topk_group, n_group,
+                topk);
+  if (group_top != 1 && !(group_top == 2 && gsize >= 2))
+    return fail(DG_ERR_SHAPE, "group_top=%d must be 1, or 2 with groups of at least two experts", group_top);
+  if (!(scale == scale) || scale - scale != 0.0f) return fail(DG_ERR_SHAPE, "scale must be finite");
+  if (T == 0) return DG_OK;
+  DeviceInfo di;
+  if ((r = device_info(&di))) return r;
+  GateArgs p = {};
+  p.logits = logits;
+  p.bias = bias;
+  p.T = T;
+  p.E = num_experts;
+  p.topk = topk;
+  p.n_group = topk_group == n_group ? 1 : n_group;  // every group stays: no group is looked at
+  p.topk_group = topk_group;
+  p.group_top = group_top;
+  p.sigmoid = score_func == DG_SCORE_SIGMOID;
+  p.renorm = renormalize;
+  p.scale = scale;
+  p.ids = topk_ids;
+  p.weights = topk_weights;
+  auto st = static_cast<cudaStream_t>(stream);
+  if (logits_dtype == 0) DG_CUDA_TRY(launch_gate<__nv_bfloat16>(p, st));
+  else DG_CUDA_TRY(launch_gate<float>(p, st));
+  return DG_OK;
+}
+
+int dg_moe_gate_backward(const void* logits, int logits_dtype, const int32_t* topk_ids, const float* d_weights, int T,
+                         int num_experts, int topk, int score_func, int renormalize, float scale, void* d_logits,
+                         void* stream) {
+  int r = check_gate(logits, logits_dtype, topk_ids, d_weights, d_logits, T, num_experts, topk, score_func, renormalize);
+  if (r) return r;
+  if (T != 0 && d_logits == logits) return fail(DG_ERR_UNSUPPORTED, "d_logits must not be logits itself");
+  if (!(scale == scale) || scale - scale != 0.0f) return fail(DG_ERR_SHAPE, "scale must be finite");
+  if (T == 0) return DG_OK;
+  DeviceInfo di;
+  if ((r = device_info(&di))) return r;
+  GateBackwardArgs p = {};
+  p.logits = logits;
+  p.ids = topk_ids;
+  p.d_weights = d_weights;
+  p.T = T;
+  p.E = num_experts;
+  p.topk = topk;
+  p.sigmoid = score_func == DG_SCORE_SIGMOID;
+  p.renorm = renormalize;
+  p.scale = scale;
+  p.d_logits = d_logits;
+  auto st = static_cast<cudaStream_t>(stream);
+  if (logits_dtype == 0) DG_CUDA_TRY(launch_gate_backward<__nv_bfloat16>(p, st));
+  else DG_CUDA_TRY(launch_gate_backward<float>(p, st));
+  return DG_OK;
 }
 
 }  // extern "C"

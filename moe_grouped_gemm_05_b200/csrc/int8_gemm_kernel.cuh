@@ -1,0 +1,390 @@
+// Warp-specialised, persistent int8 GEMM for sm_100a, dense and M-grouped:
+//
+//   D[m,n] = sa[m] * sb[n] * sum_k A[m,k] B[n,k]      (BF16 or FP32 out)
+//
+// A and B are int8, K-contiguous; sa is one FP32 scale per row of A (token),
+// sb one per row of B (output channel).  tcgen05.mma kind::i8 sums the
+// products exactly in int32 in tensor memory (the host keeps 128 * 128 * K
+// below 2^31), so the only roundings are those of the epilogue: the sum to
+// FP32, the two products with the scales, and BF16.
+//
+// Unlike the block-scaled FP8 kernel there are no scales to bring into tensor
+// memory: two accumulators of 256 columns fill it, and the issuing thread has
+// nothing to do but four MMAs and a commit for every 128 of K.  Roles (one
+// CTA per SM, persistent over output tiles):
+//   warp 0     TMEM owner; one thread issues the MMAs (of the pair's first CTA)
+//   warp 1     producer: TMA loads of A/B K-blocks into a STAGES-deep ring
+//   warps 2-9  epilogue: tcgen05.ld, scaling, swizzled staging + TMA store of
+//              fully valid 32-row slices, predicated stores for the others
+// CTAS = 2: a cluster of two CTAs computes a 256 x BN tile (cta_group::2), each
+// loading its own 128 rows of A and half of B's.  No load is multicast.
+// A K that is no multiple of 128 ends in a block that the TMA fills with zeros.
+#pragma once
+#include <cuda_bf16.h>
+#include <cstdint>
+
+#include "fp8_gemm_kernel.cuh"
+#include "ptx.cuh"
+
+namespace dg {
+
+constexpr int kInt8Threads = 32 * 10;
+constexpr int kInt8Epi0 = 2;  // first epilogue warp
+
+struct Int8Args : GemmArgs {
+  const float* sa;  // [G][rows] (masked) or [rows]
+  const float* sb;  // [G][N]
+};
+
+template <int BN, int STAGES, int MODE, int CTAS>
+struct Int8Layout {
+  static constexpr int kTileM = 128 * CTAS;
+  static constexpr int kBRows = BN / CTAS;
+  static constexpr int kABytes = 128 * kBK;
+  static constexpr int kBBytes = kBRows * kBK;
+  static constexpr int kEpiBuf = 32 * 32 * 2;  // 32 rows x 32 BF16 (or x 16 FP32)
+  static constexpr int kAccStride = BN;
+  static constexpr int kTmemCols = 512;
+  static constexpr int kOffB = STAGES * kABytes;
+  static constexpr int kOffEpi = kOffB + STAGES * kBBytes;
+  static constexpr int kOffBar = kOffEpi + 8 * kEpiBuf;
+  static constexpr int kNumBars = 2 * STAGES + 2 * 2 + 1;
+  static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
+  static constexpr int kOffGroups = kOffMisc + 16;
+  static constexpr int kGroupsBytes = MODE == MODE_MASKED                   ? (2 * kMaxMaskedGroups + 1) * 4
+                                      : (MODE == MODE_CONTIG && CTAS == 2) ? (kMaxContigBlocks + 1) * 4
+                                                                           : 0;
+  static constexpr int kSmemBytes = kOffGroups + kGroupsBytes + 1024;
+  static_assert(kSmemBytes <= kMaxSmem, "shared-memory budget exceeded");
+  static_assert(BN % 32 == 0 && BN <= 256 && 2 * kAccStride <= kTmemCols, "two accumulators fit in tensor memory");
+  static_assert(kOffEpi % 1024 == 0 && kBBytes % 1024 == 0, "swizzle atoms are 1024-byte aligned");
+};
+
+template <int BN, int STAGES, int MODE, int CTAS, bool OUT_F32>
+__global__ void __launch_bounds__(kInt8Threads, 1)
+    int8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                     const __grid_constant__ CUtensorMap tm_d, const Int8Args p) {
+  using L = Int8Layout<BN, STAGES, MODE, CTAS>;
+  constexpr bool kPair = CTAS == 2;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(smem + L::kOffBar);
+  uint64_t* empty_bar = full_bar + STAGES;
+  uint64_t* tmem_full = full_bar + 2 * STAGES;
+  uint64_t* tmem_empty = tmem_full + 2;
+  uint64_t* final_bar = tmem_full + 4;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
+  uint32_t* peer_loads = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 8);  // written by the pair's second CTA
+  int* prefix = reinterpret_cast<int*>(smem + L::kOffGroups);
+  int* counts = prefix + kMaxMaskedGroups + 1;
+  uint32_t it = 0;  // loads issued (producer warp)
+
+  const int warp = threadIdx.x / 32;
+  const int lane = threadIdx.x % 32;
+  const int num_kb = (p.K + kBK - 1) / kBK;
+  const uint32_t rank = kPair ? cluster_cta_rank() : 0;
+  const int unit0 = kPair ? static_cast<int>(blockIdx.x / 2) : static_cast<int>(blockIdx.x);
+  const int units = kPair ? static_cast<int>(gridDim.x / 2) : static_cast<int>(gridDim.x);
+
+  // ---------------------------------------------------------------- set-up
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(&full_bar[s], CTAS);
+      mbar_init(&empty_bar[s], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&tmem_full[i], 1);
+      mbar_init(&tmem_empty[i], 8 * CTAS);
+    }
+    mbar_init(final_bar, 1);
+    *abort_flag = 0;
+    fence_barrier_init();
+    prefetch_tensormap(&tm_a);
+    prefetch_tensormap(&tm_b);
+    prefetch_tensormap(&tm_d);
+  }
+  __syncwarp();
+  if (warp == 0) {
+    tmem_alloc<CTAS>(tmem_holder, L::kTmemCols);
+    tmem_relinquish<CTAS>();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  if (MODE == MODE_MASKED && warp == kInt8Epi0) masked_tile_prefix<L::kTileM>(p, prefix, counts, lane);
+  if (MODE == MODE_CONTIG && kPair && warp == kInt8Epi0) contig_pair_table(p, prefix, lane);
+  tc_fence_before();
+  if constexpr (kPair) cluster_sync(); else __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  const int ntiles = total_tiles<MODE, CTAS>(p, prefix);
+
+  if (warp == 1) {
+    // ============================================================ producer
+    const uint32_t full0 = kPair ? mapa_shared(smem_u32(full_bar), 0) : smem_u32(full_bar);
+    bool ok = true;
+    for (int t = unit0; t < ntiles && ok; t += units) {
+      const Tile tl = tile_of<MODE, L::kTileM>(t, p, prefix, counts);
+      int grp_a = 0, grp_b = 0;
+      if (MODE == MODE_CONTIG) {
+        grp_b = contig_expert<CTAS>(tl, p);
+        if (grp_b < 0) continue;
+      } else if (MODE == MODE_MASKED) {
+        grp_a = grp_b = tl.g;
+      }
+      const int m_base = tl.row0 + 128 * static_cast<int>(rank);
+      const int n0 = tl.n_blk * BN;
+      // each CTA of a pair holds half of the tile's MMA width of B
+      const int b_row = n0 + static_cast<int>(rank) * (tile_mma_n<BN, CTAS, 0>(n0, p.N) / CTAS);
+      for (int kb = 0; kb < num_kb; ++kb, ++it) {
+        const uint32_t s = it % STAGES;
+        ok = wait_phase<false>(&empty_bar[s], ((it / STAGES) & 1) ^ 1, abort_flag, p.wait_limit_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          uint8_t* a_dst = smem + s * L::kABytes;
+          uint8_t* b_dst = smem + L::kOffB + s * L::kBBytes;
+          if constexpr (kPair) {
+            tma_load_3d_pair(a_dst, &tm_a, full0 + 8 * s, kb * kBK, m_base, grp_a);
+            tma_load_3d_pair(b_dst, &tm_b, full0 + 8 * s, kb * kBK, b_row, grp_b);
+            mbar_arrive_expect_tx_cluster(full0 + 8 * s, L::kABytes + L::kBBytes);
+          } else {
+            tma_load_3d(a_dst, &tm_a, &full_bar[s], kb * kBK, m_base, grp_a);
+            tma_load_3d(b_dst, &tm_b, &full_bar[s], kb * kBK, b_row, grp_b);
+            mbar_arrive_expect_tx(&full_bar[s], L::kABytes + L::kBBytes);
+          }
+        }
+      }
+    }
+    // Every load must land before its CTA exits: alone, the last STAGES loads
+    // are waited for here; in a pair all loads signal the first CTA, which
+    // drains both after the cluster barrier of the teardown.
+    if constexpr (!kPair) {
+      if (lane == 0) {
+        for (uint32_t i = it > STAGES ? it - STAGES : 0; i < it; ++i)
+          wait_phase_drain(&full_bar[i % STAGES], (i / STAGES) & 1);
+      }
+    } else if (rank == 1 && lane == 0) {
+      st_shared_cluster_u32(mapa_shared(smem_u32(peer_loads), 0), it);
+    }
+    __syncwarp();
+  } else if (warp == 0) {
+    // ============================================================ MMA issuer
+    if ((!kPair || rank == 0) && lane == 0) {
+      const uint64_t a0 = make_smem_desc(smem_u32(smem), 16, 1024, 2);
+      const uint64_t b0 = make_smem_desc(smem_u32(smem + L::kOffB), 16, 1024, 2);
+      const uint32_t full_base = smem_u32(full_bar), empty_base = smem_u32(empty_bar);
+      uint32_t s = 0, phase = 0, own = 0;
+      bool ok = true;
+      const bool ragged_n = p.N % BN != 0;
+      for (int t = unit0; t < ntiles && ok; t += units) {
+        int mma_n = BN;
+        if (MODE == MODE_CONTIG || ragged_n) {
+          const Tile tl = tile_of<MODE, L::kTileM>(t, p, prefix, counts);
+          if (MODE == MODE_CONTIG && contig_expert<CTAS>(tl, p) < 0) continue;
+          mma_n = tile_mma_n<BN, CTAS, 0>(tl.n_blk * BN, p.N);
+        }
+        const uint32_t idesc = make_idesc_i8(L::kTileM, mma_n);
+        const uint32_t acc = own & 1, use = own >> 1;
+        ++own;
+        if (!mbar_try_wait(&tmem_empty[acc], (use & 1) ^ 1))
+          ok = wait_phase<false>(&tmem_empty[acc], (use & 1) ^ 1, abort_flag, p.wait_limit_ns);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * L::kAccStride;
+        uint32_t accumulate = 0;
+        for (int kb = 0; kb < num_kb; ++kb) {
+          if (!mbar_try_wait_addr(full_base + 8 * s, phase)) {
+            ok = wait_phase<false>(&full_bar[s], phase, abort_flag, p.wait_limit_ns);
+            if (!ok) break;
+          }
+          tc_fence_after();
+          const uint64_t a = a0 + s * (L::kABytes >> 4), b = b0 + s * (L::kBBytes >> 4);
+          mma_i8<CTAS>(d_tmem, a, b, idesc, accumulate);
+          mma_i8<CTAS>(d_tmem, a + 2, b + 2, idesc, 1u);
+          mma_i8<CTAS>(d_tmem, a + 4, b + 4, idesc, 1u);
+          mma_i8<CTAS>(d_tmem, a + 6, b + 6, idesc, 1u);
+          accumulate = 1;
+          if constexpr (kPair) tc_commit_pair_addr(empty_base + 8 * s);
+          else tc_commit_addr<1>(empty_base + 8 * s);
+          if (++s == STAGES) {
+            s = 0;
+            phase ^= 1;
+          }
+        }
+        if (!ok) break;
+        if constexpr (kPair) tc_commit_pair(&tmem_full[acc]);
+        else tc_commit<1>(&tmem_full[acc]);
+      }
+      // all MMAs issued here complete before TMEM is freed
+      tc_commit<CTAS>(final_bar);
+      wait_phase_drain(final_bar, 0);
+    }
+    __syncwarp();
+  } else {
+    // ============================================================ epilogue
+    // Two warps per TMEM lane quarter, one on the even, one on the odd
+    // 32-column chunks; the next chunk's tcgen05.ld is in flight while the
+    // current one is scaled and stored.
+    const int q = warp % 4;
+    const int epi = warp - kInt8Epi0;
+    const int half = epi >> 2;
+    uint8_t* buf = smem + L::kOffEpi + epi * L::kEpiBuf;
+    const uint32_t empty0 = kPair ? mapa_shared(smem_u32(tmem_empty), 0) : smem_u32(tmem_empty);
+    constexpr int kChunks = BN / 32;
+    constexpr int kMine = kChunks / 2;
+    static_assert(kChunks % 2 == 0, "both warps of a quarter take the same number of chunks");
+    uint32_t own = 0;
+    for (int t = unit0; t < ntiles; t += units) {
+      const Tile tl = tile_of<MODE, L::kTileM>(t, p, prefix, counts);
+      int expert = 0, own_e = 0;
+      if (MODE == MODE_CONTIG) {
+        const int own_blk = tl.row0 / 128 + static_cast<int>(rank);  // a pair's blocks may differ in expert
+        own_e = own_blk < p.rows / 128 ? __ldg(&p.m_indices[own_blk * 128]) : -1;
+        if ((own_e < -1 || own_e >= p.G) && warp == kInt8Epi0 && lane == 0 && tl.n_blk == 0) atomicOr(&g_dg_error, 0x2);
+        expert = contig_expert<CTAS>(tl, p);
+        if (expert < 0) continue;
+      } else if (MODE == MODE_MASKED) {
+        expert = tl.g;
+      }
+      const uint32_t acc = own & 1, use = own >> 1;
+      ++own;
+      const int row0 = tl.row0 + 128 * static_cast<int>(rank) + 32 * q;  // the warp's first row
+      const int m = row0 + lane;
+      bool valid;
+      if (MODE == MODE_DENSE) {
+        valid = m < p.rows;
+      } else if (MODE == MODE_CONTIG) {
+        const int idx = m < p.rows ? __ldg(&p.m_indices[m]) : -1;
+        valid = own_e == expert && idx == expert;
+        if (own_e == expert && idx != expert && idx != -1 && tl.n_blk == 0 && half == 0)
+          atomicOr(&g_dg_error, (idx >= 0 && idx < p.G) ? 0x8 : 0x2);
+      } else {
+        valid = m < counts[tl.g];
+      }
+      const bool all_valid = __all_sync(0xffffffffu, valid);
+      const bool any_valid = __any_sync(0xffffffffu, valid);
+      const int n0 = tl.n_blk * BN;
+      const int zd = MODE == MODE_MASKED ? tl.g : 0;
+      const size_t row_g = static_cast<size_t>(zd) * p.rows + m;
+      const float sa = valid ? __ldg(p.sa + row_g) : 0.0f;
+      const float* sb = p.sb + static_cast<size_t>(expert) * p.N;
+      const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * L::kAccStride;
+
+      bool ok = wait_phase<false>(&tmem_full[acc], use & 1, abort_flag, p.wait_limit_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+
+      // 16 columns of 64 bytes a row (FP32), or 32 columns (BF16), by TMA or by each lane for its row
+      auto store64 = [&](const uint4 (&w)[4], int col, void* d_row, int per16) {
+        if (all_valid) {
+          if (lane == 0) bulk_wait_group_read<0>();  // the previous store has read the buffer
+          __syncwarp();
+          uint8_t* rowp = buf + lane * 64;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4*>(rowp + (i ^ ((lane >> 1) & 3)) * 16) = w[i];
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tm_d, buf, col, row0, zd);
+            bulk_commit_group();
+          }
+        } else if (valid) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (col + per16 * i < p.N) static_cast<uint4*>(d_row)[i] = w[i];
+        }
+      };
+      auto finish = [&](uint32_t (&r)[32], int col0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 b = col0 + 4 * i < p.N ? __ldg(reinterpret_cast<const float4*>(sb + col0) + i)
+                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+          r[4 * i] = __float_as_uint(__int2float_rn(static_cast<int>(r[4 * i])) * sa * b.x);
+          r[4 * i + 1] = __float_as_uint(__int2float_rn(static_cast<int>(r[4 * i + 1])) * sa * b.y);
+          r[4 * i + 2] = __float_as_uint(__int2float_rn(static_cast<int>(r[4 * i + 2])) * sa * b.z);
+          r[4 * i + 3] = __float_as_uint(__int2float_rn(static_cast<int>(r[4 * i + 3])) * sa * b.w);
+        }
+        uint4 w[4];
+        if constexpr (OUT_F32) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int col = col0 + 16 * h;
+            if (col >= p.N) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              w[i] = make_uint4(r[16 * h + 4 * i], r[16 * h + 4 * i + 1], r[16 * h + 4 * i + 2], r[16 * h + 4 * i + 3]);
+            store64(w, col, p.d32 + row_g * p.N + col, 4);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t h[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(r[8 * i + 2 * j]),
+                                                             __uint_as_float(r[8 * i + 2 * j + 1]));
+              h[j] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            w[i] = make_uint4(h[0], h[1], h[2], h[3]);
+          }
+          store64(w, col0, p.d + row_g * p.N + col0, 8);
+        }
+      };
+
+      if (any_valid) {
+        uint32_t r[2][32];
+        if (n0 + 32 * half < p.N) tmem_ld_32x32b_x32(t_row + 32 * half, r[0]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int c = half + 2 * i;
+          const int col0 = n0 + 32 * c;
+          if (col0 >= p.N) break;
+          if (i + 1 < kMine && col0 + 64 < p.N) tmem_ld_32x32b_x32(t_row + 32 * (c + 2), r[(i + 1) & 1]);
+          finish(r[i & 1], col0);
+          tmem_wait_ld();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (kPair) mbar_arrive_remote(empty0 + 8 * acc);
+        else mbar_arrive(&tmem_empty[acc]);
+      }
+    }
+    // the staging buffers must have been read before the CTA exits
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+  }
+
+  // ---------------------------------------------------------------- teardown
+  tc_fence_before();
+  if constexpr (kPair) {
+    cluster_sync();  // both CTAs have stopped issuing; the second CTA's load count is visible
+    if (rank == 0 && warp == 1 && lane == 0) {
+      // A CTA that gave up before issuing load j never arrives: arrive in its
+      // place, then wait for the loads that were issued.
+      const uint32_t it1 = *reinterpret_cast<volatile uint32_t*>(peer_loads);
+      const uint32_t hi = it > it1 ? it : it1;
+      for (uint32_t j = hi > STAGES ? hi - STAGES : 0; j < hi; ++j) {
+        uint64_t* b = &full_bar[j % STAGES];
+        if (j >= it) mbar_arrive(b);
+        if (j >= it1) mbar_arrive(b);
+        wait_phase_drain(b, (j / STAGES) & 1);
+      }
+    }
+    __syncwarp();
+    cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc<CTAS>(tmem_base, L::kTmemCols);
+  }
+}
+
+}  // namespace dg

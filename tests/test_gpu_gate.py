@@ -1,0 +1,308 @@
+"""GPU parity of the expert routing (the same experts as a choice in 64 bits,
+weights within their rounding) and of its gradient, against oracle.routing.
+
+Tolerances, with u = 2^-24 and D the spread of the finite logits that a row's
+weights are made of: exp is within 2u of its argument's, whose subtraction
+adds D u; a sum over E terms adds at most (ceil(E / 32) + 5) u; quotient and
+scale one u each.  Numerator and denominator then give (2D + E/32 + 13) u, and
+the sigmoid's own quotient 4u more.  A gradient's terms carry that error twice
+(the share and the mean's shares) and 12u of their own sums and products, all
+relative to the sum of their magnitudes; a BF16 result half a step more.
+"""
+import numpy as np
+import pytest
+import torch
+
+from moe_grouped_gemm_05_b200 import binding as dg
+from oracle import routing
+
+pytestmark = pytest.mark.gpu
+INF = float("inf")
+U = 2.0 ** -24
+
+
+@pytest.fixture(autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    dg.get_device_error()
+
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+def _slack(l, score):
+    """Relative error of a weight per row, in units of U (see above)."""
+    finite = np.where(np.isfinite(l), l, np.nan)
+    with np.errstate(all="ignore"):
+        import warnings
+        with warnings.catch_warnings():
+            warnings.simplefilter("ignore")
+            spread = np.nan_to_num(np.nanmax(finite, axis=1) - np.nanmin(finite, axis=1))
+    # terms further than 110 below the largest are zero in both
+    return 2 * np.minimum(spread, 110.0) + -(-l.shape[1] // 32) + 17
+
+
+def check_gate(logits, topk, bias=None, **kw):
+    logits = logits.cuda()
+    bias = None if bias is None else bias.float().cuda()
+    ids, w = dg.moe_gate(logits, topk, bias, **kw)
+    torch.cuda.synchronize()
+    l = _f64(logits)
+    ref_ids, ref_w, bad = routing.moe_gate(l, topk, None if bias is None else _f64(bias), **kw)
+    assert dg.get_device_error() == (dg.DG_DEVERR_BAD_LOGIT if bad.any() else 0)
+    got = ids.cpu().numpy()
+    assert np.array_equal(got, ref_ids), np.argwhere(got != ref_ids)[:4]
+    tol = U * _slack(l, kw.get("score", "softmax"))[:, None] * np.abs(ref_w) + 2.0 ** -126
+    err = np.abs(_f64(w) - ref_w)
+    assert (err <= tol).all(), (err / np.maximum(np.abs(ref_w), 1e-300)).max() / U
+    return ids, w
+
+
+def _rand(T, E, seed, dtype=torch.float32, sigma=1.5):
+    rng = np.random.default_rng(seed)
+    return torch.from_numpy(sigma * rng.standard_normal((T, E))).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,topk", [(1, 1, 1), (3, 2, 2), (5, 7, 3), (129, 32, 8), (64, 33, 4), (70, 60, 6),
+                                      (33, 64, 1), (40, 100, 32), (200, 256, 8), (9, 257, 5), (17, 512, 16),
+                                      (6, 1000, 7), (12, 1024, 32)])
+def test_plain_choice(T, E, topk, score, dtype):
+    l = _rand(T, E, T * 1000 + E, dtype)
+    check_gate(l, topk, score=score)
+    check_gate(l, topk, score=score, renormalize=True, scale=2.5)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,topk", [(1, 8, 2), (300, 64, 6), (50, 130, 9), (400, 256, 8), (20, 1024, 32)])
+def test_biased_choice(T, E, topk, score, dtype):
+    l = _rand(T, E, T + E, dtype)
+    b = 0.05 * _rand(1, E, 5)[0]
+    check_gate(l, topk, b, score=score, renormalize=True)
+    check_gate(l, topk, torch.zeros(E), score=score)      # equal logits tie exactly: the lowest index
+
+
+@pytest.mark.parametrize("group_top", [1, 2])
+@pytest.mark.parametrize("score,biased", [("softmax", False), ("sigmoid", True), ("sigmoid", False)])
+@pytest.mark.parametrize("T,E,topk,n_group,topk_group", [
+    (300, 256, 8, 8, 4), (40, 64, 4, 4, 2), (100, 160, 6, 8, 3), (50, 60, 4, 6, 2), (30, 256, 8, 32, 3),
+    (20, 1024, 16, 16, 5), (25, 66, 3, 3, 1), (30, 16, 2, 8, 8), (10, 96, 8, 2, 1), (64, 512, 8, 4, 2)])
+def test_groups(T, E, topk, n_group, topk_group, score, biased, group_top):
+    """Groups that are whole lanes of the warp and those that are not."""
+    b = 0.05 * _rand(1, E, 9)[0] if biased else None
+    check_gate(_rand(T, E, T + 7 * E), topk, b, score=score, n_group=n_group, topk_group=topk_group,
+               group_top=group_top, renormalize=True, scale=2.5)
+    check_gate(_rand(T, E, T + 8 * E, torch.bfloat16), topk, b, score=score, n_group=n_group, topk_group=topk_group,
+               group_top=group_top)
+
+
+def test_large_batch_and_ragged_tail():
+    check_gate(_rand(20001, 64, 3, torch.bfloat16), 6, score="softmax", renormalize=True)
+    check_gate(_rand(4099, 256, 4), 8, 0.05 * _rand(1, 256, 6)[0], score="sigmoid", n_group=8, topk_group=4,
+               group_top=2, renormalize=True, scale=2.5)
+
+
+def test_scores_that_32_bits_cannot_tell_apart():
+    """Biases that bring every expert's score to nearly the same value: the
+    order is decided by differences of about 2^-26, far below what the scores'
+    32-bit values resolve, and the kernel still chooses as in 64 bits."""
+    T, E = 64, 256
+    for score in ("sigmoid", "softmax"):
+        l = _rand(1, E, 21).repeat(T, 1)
+        s = routing.scores(_f64(l[:1]), score)[0]
+        b = torch.from_numpy((1.0 - s).astype(np.float32))
+        check_gate(l, 8, b, score=score, renormalize=True)
+        check_gate(l, 8, b, score=score, n_group=8, topk_group=4, group_top=2)
+        check_gate(l, 8, b, score=score, n_group=4, topk_group=1, group_top=1)
+    # a saturated sigmoid: every score is 1 in 32 bits
+    l = 20.0 + _rand(50, 96, 22).abs() / 64
+    check_gate(l, 8, torch.zeros(96), score="sigmoid")
+
+
+def test_masks_and_padding():
+    T, E, topk = 40, 64, 6
+    l = _rand(T, E, 31)
+    l[torch.rand(T, E, generator=torch.Generator().manual_seed(1)) < 0.9] = -INF   # fewer experts than slots
+    l[3] = -INF                                                                  # a padded token
+    l[4, 1:] = -INF                                                              # one expert left
+    l[5] = torch.finfo(torch.float32).min                                        # the lowest finite value: not masked
+    l[6, ::2] = torch.finfo(torch.float32).min
+    l[7] = -0.0
+    l[7, ::3] = 0.0                                                              # -0 and 0 tie
+    b = torch.zeros(E)
+    b[10] = -INF
+    for kw in (dict(score="softmax"), dict(score="sigmoid"), dict(score="softmax", renormalize=True),
+               dict(score="sigmoid", renormalize=True), dict(score="sigmoid", renormalize=True, n_group=8, topk_group=2),
+               dict(score="softmax", n_group=8, topk_group=3, group_top=2)):
+        ids, w = check_gate(l, topk, **kw)
+        assert (ids[3] == -1).all() and (w[3] == 0).all()
+        ids, _ = check_gate(l, topk, b, **kw)
+        assert not (ids == 10).any()
+    ids, w = dg.moe_gate(torch.full((3, E), -INF, device="cuda"), topk, score="sigmoid", renormalize=True)
+    assert (ids == -1).all() and (w == 0).all()
+
+
+@pytest.mark.parametrize("what", [float("nan"), INF])
+def test_rows_that_are_not_numbers_are_not_routed(what):
+    l = _rand(10, 60, 41)
+    l[4, 59] = what
+    l[9, 0] = what
+    for score in ("softmax", "sigmoid"):
+        ids, w = check_gate(l, 4, score=score, renormalize=True)
+        assert (ids[4] == -1).all() and (w[9] == 0).all() and (ids[5] >= 0).all()
+    b = torch.zeros(60)
+    b[7] = what
+    ids, _ = check_gate(_rand(10, 60, 42), 4, b, score="sigmoid")
+    assert (ids == -1).all()
+
+
+def test_extreme_logits():
+    E = 48
+    l = torch.linspace(-3e38, 3e38, 32 * E).reshape(32, E)
+    check_gate(l, 8, score="softmax", renormalize=True)
+    check_gate(l, 8, score="sigmoid", renormalize=True)
+    l = -200.0 - _rand(32, E, 51).abs()           # every sigmoid is zero in 32 bits
+    check_gate(l, 8, score="sigmoid", renormalize=True, scale=2.5)
+    check_gate(200.0 + _rand(32, E, 52), 8, score="sigmoid", renormalize=True)
+    check_gate(l, 8, torch.zeros(E), score="sigmoid")
+
+
+def test_outputs_beyond_the_rows_stay_and_no_tokens_is_nothing():
+    ids = torch.full((12, 3), 77, dtype=torch.int32, device="cuda")
+    w = torch.full((12, 3), 77.0, device="cuda")
+    dg.moe_gate(_rand(5, 9, 61).cuda(), 3, ids=ids[:5], weights=w[:5])
+    torch.cuda.synchronize()
+    assert (ids[5:] == 77).all() and (w[5:] == 77).all() and (ids[:5] < 9).all()
+    i0, w0 = dg.moe_gate(torch.empty((0, 9), device="cuda"), 3)
+    assert i0.shape == (0, 3) and w0.shape == (0, 3)
+    assert dg.moe_gate_backward(torch.empty((0, 9), device="cuda"), i0, w0).shape == (0, 9)
+
+
+# ------------------------------------------------------------------ gradient
+
+
+def check_backward(logits, ids, g, flag=0, **kw):
+    logits, ids, g = logits.cuda(), ids.to(torch.int32).cuda(), g.float().cuda()
+    out = torch.full_like(logits, 7.0)
+    dg.moe_gate_backward(logits, ids, g, d_logits=out, **kw)
+    torch.cuda.synchronize()
+    assert dg.get_device_error() == flag
+    l = _f64(logits)
+    ref, size = routing.moe_gate_backward(l, ids.cpu().numpy(), _f64(g), **kw)
+    tol = (2 * _slack(l, kw.get("score")) + 18)[:, None] * U * size + 2.0 ** -126
+    if logits.dtype == torch.bfloat16:
+        tol = tol + 2.0 ** -8 * (np.abs(ref) + tol)
+    err = np.abs(_f64(out) - ref)
+    assert (err <= tol).all(), np.argwhere(err > tol)[:4]
+    again = dg.moe_gate_backward(logits, ids, g, **kw)
+    assert torch.equal(again, out)
+    return out
+
+
+def _ids(T, E, topk, seed, drop=0.0):
+    rng = np.random.default_rng(seed)
+    ids = np.stack([rng.permutation(E)[:topk] for _ in range(T)]).astype(np.int32)
+    ids[rng.random((T, topk)) < drop] = -1
+    return torch.from_numpy(ids)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+@pytest.mark.parametrize("T,E,topk", [(1, 1, 1), (3, 2, 2), (5, 7, 3), (129, 32, 8), (64, 33, 4), (77, 60, 4),
+                                      (40, 100, 32), (200, 256, 8), (9, 257, 5), (17, 512, 16), (12, 1024, 32)])
+def test_gradient(T, E, topk, score, renormalize, dtype):
+    check_backward(_rand(T, E, T + E, dtype), _ids(T, E, topk, T, 0.1), _rand(T, topk, E), score=score,
+                   renormalize=renormalize, scale=2.5)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalize", [False, True])
+def test_gradient_edges(score, renormalize):
+    T, E, topk = 12, 40, 4
+    l, ids, g = _rand(T, E, 71), _ids(T, E, topk, 72), _rand(T, topk, 73)
+    l[0] = -INF
+    ids[0] = -1                               # a padded token
+    ids[1] = -1
+    l[1, 0] = float("nan")                    # not routed: zeros whatever its logits are
+    l[2, 20:] = -INF
+    ids[2] = torch.tensor([0, 3, 19, -1])     # masked experts, one slot left over
+    ids[3] = torch.tensor([5, 5, 7, 5])       # one expert in three slots
+    l[4] = -200.0 - l[4].abs()                # scores that are zero in 32 bits
+    l[5] = 60.0
+    g[6] = 0.0
+    out = check_backward(l[2:], ids[2:], g[2:], score=score, renormalize=renormalize, scale=1.0)
+    assert (out[4] == 0).all()
+    out = dg.moe_gate_backward(l.cuda(), ids.int().cuda(), g.cuda(), score=score, renormalize=renormalize)
+    assert (out[:2] == 0).all() and dg.get_device_error() == 0
+
+
+def test_gradient_flags_ids_out_of_range():
+    l, g = _rand(3, 8, 81), _rand(3, 2, 82)
+    bad = torch.tensor([[0, 8], [1, -2], [3, 4]])
+    out = check_backward(l, bad, g, flag=dg.DG_DEVERR_BAD_EXPERT, score="sigmoid", renormalize=True)
+    assert out[0, 1:].eq(0).all()
+
+
+def test_gradient_of_the_weights_by_differences():
+    """The whole path against central differences of the forward kernel's own
+    weights, in directions that leave the choice as it is."""
+    T, E, topk = 50, 24, 4
+    l = _rand(T, E, 91).cuda()
+    g = _rand(T, topk, 92).cuda()
+    v = _rand(T, E, 93).cuda()
+    h = 2.0 ** -7
+    for score in ("softmax", "sigmoid"):
+        for renormalize in (False, True):
+            kw = dict(score=score, renormalize=renormalize, scale=2.5)
+            ids, _ = dg.moe_gate(l, topk, **kw)
+            d = dg.moe_gate_backward(l, ids, g, **kw)
+            iu, wu = dg.moe_gate(l + h * v, topk, **kw)
+            il, wl = dg.moe_gate(l - h * v, topk, **kw)
+            same = ((iu == ids) & (il == ids)).all(dim=1)
+            assert same.sum() > T // 2
+            by_difference = ((wu - wl).double() * g).sum(1) / (2 * h)
+            by_gradient = (d.double() * v).sum(1)
+            # third derivatives along v: at most 2.5 * |g|_1 * |v|_max^3 * 1 each, times h^2 / 6; rounding
+            # of the weights (at most 2.5 * 2^-20 each) over h
+            bound = g.abs().sum(1).double() * (2.5 * v.abs().amax(1).double() ** 3 * h * h + 2.5 * 2.0 ** -19 / h)
+            assert ((by_difference - by_gradient).abs()[same] <= bound[same]).all()
+
+
+# ------------------------------------------------------------------ streams and graphs
+
+
+def test_two_streams_and_a_captured_graph():
+    T, E, topk = 300, 256, 8
+    kw = dict(score="sigmoid", n_group=8, topk_group=4, group_top=2, renormalize=True, scale=2.5)
+    b = (0.05 * _rand(1, E, 3)[0]).cuda()
+    one, two = _rand(T, E, 1).cuda(), _rand(T, E, 2).cuda()
+    want = [dg.moe_gate(x, topk, b, **kw) for x in (one, two)]
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for s, x in ((s1, one), (s2, two)):
+        with torch.cuda.stream(s):
+            got.append(dg.moe_gate(x, topk, b, **kw))
+    torch.cuda.synchronize()
+    for (i, w), (gi, gw) in zip(want, got):
+        assert torch.equal(i, gi) and torch.equal(w, gw)
+    # forward and gradient captured once, replayed on new inputs
+    x, g = one.clone(), _rand(T, topk, 4).cuda()
+    ids = torch.empty((T, topk), dtype=torch.int32, device="cuda")
+    w, d = torch.empty((T, topk), device="cuda"), torch.empty_like(x)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        dg.moe_gate(x, topk, b, ids=ids, weights=w, **kw)
+        dg.moe_gate_backward(x, ids, g, score="sigmoid", renormalize=True, scale=2.5, d_logits=d)
+    for src, (i, ww) in zip((one, two), want):
+        x.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ids, i) and torch.equal(w, ww)
+        assert torch.equal(d, dg.moe_gate_backward(src, i, g, score="sigmoid", renormalize=True, scale=2.5))
+    assert dg.get_device_error() == 0

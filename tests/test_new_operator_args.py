@@ -1,0 +1,123 @@
+"""Refusals of the routing and int8 entry points, on the host (no GPU)."""
+import ctypes
+
+import pytest
+import torch
+
+from moe_grouped_gemm_05_b200 import binding as dg
+from moe_grouped_gemm_05_b200 import build
+
+P = ctypes.c_void_p
+GOOD, NULL, ODD8, ODD2 = P(0x10000), P(0), P(0x10008), P(0x10002)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return dg.load()
+
+
+def test_int8_gemm_refusals(lib):
+    def dense(a=GOOD, sa=GOOD, b=GOOD, sb=GOOD, d=GOOD, M=64, N=256, K=256, f32=0):
+        return lib.dg_int8_gemm_nt(a, sa, b, sb, d, M, N, K, f32, None)
+
+    for name in ("a", "sa", "b", "sb", "d"):
+        assert dense(**{name: NULL}) == dg.DG_ERR_NULL, name
+        assert dense(**{name: ODD8}) == dg.DG_ERR_ALIGN, name
+    assert dense(K=0) == dense(K=24) == dense(K=-16) == dg.DG_ERR_SHAPE
+    assert dense(K=131072) == dg.DG_ERR_SHAPE                # 128 * 128 * K leaves int32
+    assert b"131056" in lib.dg_get_last_error()
+    assert dense(N=0) == dense(N=24) == dg.DG_ERR_SHAPE
+    assert dense(M=-1) == dg.DG_ERR_SHAPE
+    assert dense(f32=2) == dg.DG_ERR_UNSUPPORTED
+    assert dense(a=NULL, d=NULL, M=0) == 0                   # no rows: nothing to do
+
+    def contiguous(idx=GOOD, M=256, G=4, **kw):
+        return lib.dg_m_grouped_int8_gemm_nt_contiguous(kw.get("a", GOOD), GOOD, GOOD, GOOD, GOOD, idx, M,
+                                                        kw.get("N", 256), kw.get("K", 256), G, None)
+
+    assert contiguous(idx=NULL) == dg.DG_ERR_NULL and contiguous(a=ODD8) == dg.DG_ERR_ALIGN
+    assert contiguous(M=200) == contiguous(G=0) == contiguous(K=20) == contiguous(M=-128) == dg.DG_ERR_SHAPE
+    assert contiguous(M=0) == 0
+
+    def masked(cnt=GOOD, M=256, G=4, K=256):
+        return lib.dg_m_grouped_int8_gemm_nt_masked(GOOD, GOOD, GOOD, GOOD, GOOD, cnt, G, M, 256, K, None)
+
+    assert masked(cnt=NULL) == dg.DG_ERR_NULL
+    assert masked(G=0) == masked(G=513) == masked(M=-1) == masked(K=8) == dg.DG_ERR_SHAPE
+    assert masked(M=0) == 0
+
+
+def test_quantize_refusals(lib):
+    def quantize(x=GOOD, t=0, q=GOOD, s=GOOD, M=8, K=256):
+        return lib.dg_quantize_int8_per_token(x, t, q, s, M, K, None)
+
+    assert quantize(x=NULL) == quantize(q=NULL) == quantize(s=NULL) == dg.DG_ERR_NULL
+    assert quantize(x=ODD8) == quantize(q=ODD8) == quantize(s=ODD2) == dg.DG_ERR_ALIGN
+    assert quantize(t=2) == dg.DG_ERR_UNSUPPORTED
+    assert quantize(K=8) == quantize(K=0) == quantize(M=-1) == dg.DG_ERR_SHAPE
+    assert quantize(x=NULL, M=0) == 0
+
+    def permute(ids=GOOD, T=100, topk=2, G=4, x=GOOD, t=0, K=256, a=GOOD, sa=GOOD, row_of=GOOD, cap=None):
+        c = lib.dg_moe_permute_capacity(100, 2, 4) if cap is None else cap
+        return lib.dg_moe_quantize_permute_int8(ids, T, topk, G, x, t, K, a, sa, GOOD, row_of, GOOD, c, None)
+
+    assert permute(ids=NULL) == permute(x=NULL) == permute(a=NULL) == permute(row_of=NULL) == dg.DG_ERR_NULL
+    assert permute(x=ODD8) == permute(a=ODD8) == permute(sa=ODD8) == dg.DG_ERR_ALIGN
+    assert permute(t=7) == dg.DG_ERR_UNSUPPORTED
+    assert permute(K=100) == permute(G=1025) == permute(topk=0) == permute(T=-1) == dg.DG_ERR_SHAPE
+    assert permute(cap=lib.dg_moe_permute_capacity(100, 2, 4) - 128) == dg.DG_ERR_SHAPE
+    assert permute(cap=lib.dg_moe_permute_capacity(100, 2, 4) + 64) == dg.DG_ERR_SHAPE
+
+
+def test_gate_refusals(lib):
+    def gate(l=GOOD, t=1, bias=GOOD, T=10, E=64, k=4, score=1, ng=8, kg=4, gt=2, renorm=1, scale=1.0, ids=GOOD, w=GOOD):
+        return lib.dg_moe_gate(l, t, bias, T, E, k, score, ng, kg, gt, renorm, scale, ids, w, None)
+
+    assert gate(l=NULL) == gate(ids=NULL) == gate(w=NULL) == dg.DG_ERR_NULL
+    assert gate(l=ODD8) == gate(bias=ODD8) == gate(ids=ODD2) == gate(w=ODD2) == dg.DG_ERR_ALIGN
+    assert gate(t=2) == gate(score=2) == gate(renorm=2) == dg.DG_ERR_UNSUPPORTED
+    assert gate(E=0) == gate(E=1025) == gate(T=-1) == dg.DG_ERR_SHAPE
+    assert gate(k=0) == gate(k=33) == gate(E=3, k=4, ng=1, kg=1, gt=1) == dg.DG_ERR_SHAPE
+    assert gate(ng=0) == gate(ng=7) == gate(ng=64, kg=1, gt=1, k=1) == dg.DG_ERR_SHAPE
+    assert gate(kg=0) == gate(kg=9) == gate(kg=1, k=9) == dg.DG_ERR_SHAPE
+    assert gate(gt=0) == gate(gt=3) == gate(E=8, ng=8, k=4, gt=2) == dg.DG_ERR_SHAPE
+    assert gate(scale=float("inf")) == gate(scale=float("nan")) == dg.DG_ERR_SHAPE
+    assert gate(T=0, l=NULL, ids=NULL, w=NULL) == 0
+
+    def backward(l=GOOD, t=1, ids=GOOD, g=GOOD, T=10, E=64, k=4, score=1, renorm=1, scale=1.0, d=P(0x20000)):
+        return lib.dg_moe_gate_backward(l, t, ids, g, T, E, k, score, renorm, scale, d, None)
+
+    assert backward(l=NULL) == backward(ids=NULL) == backward(g=NULL) == backward(d=NULL) == dg.DG_ERR_NULL
+    assert backward(l=ODD8) == backward(d=ODD8) == backward(g=ODD2) == dg.DG_ERR_ALIGN
+    assert backward(t=3) == backward(score=-1) == backward(renorm=-1) == dg.DG_ERR_UNSUPPORTED
+    assert backward(d=GOOD) == dg.DG_ERR_UNSUPPORTED            # in place
+    assert backward(k=65) == backward(E=2000) == backward(T=-3) == dg.DG_ERR_SHAPE
+    assert backward(scale=float("-inf")) == dg.DG_ERR_SHAPE
+    assert backward(T=0, l=NULL, d=NULL) == 0
+
+
+def test_binding_refuses_before_the_library_is_called():
+    x = torch.zeros(4, 16)
+    with pytest.raises(ValueError, match="CUDA"):
+        dg.moe_gate(x, 2)
+    with pytest.raises(TypeError, match="bfloat16"):
+        dg.moe_gate(x.half(), 2)
+    with pytest.raises(ValueError, match="score"):
+        dg.moe_gate(x, 2, score="tanh")
+    with pytest.raises(ValueError, match="CUDA"):
+        dg.quantize_int8_per_token(x)
+    with pytest.raises(TypeError, match="int8"):
+        dg.int8_gemm_nt(x, x, x, x)
+    with pytest.raises(TypeError, match="int32"):
+        dg.moe_quantize_permute_int8(x, 4, x)
+    cpu = torch.device("cpu")
+    assert dg._operand(x, (torch.float32,), (4, 16), "x", cpu) == x.data_ptr()
+    with pytest.raises(TypeError):
+        dg._operand(x, (torch.int8,), (4, 16), "x", cpu)
+    with pytest.raises(ValueError):
+        dg._operand(x, (torch.float32,), (16, 4), "x", cpu)
+    with pytest.raises(ValueError):
+        dg._operand(x.t(), (torch.float32,), (16, 4), "x", cpu)
+    with pytest.raises(ValueError):
+        dg._operand(x, (torch.float32,), (4, 16), "x", torch.device("cuda", 0))
