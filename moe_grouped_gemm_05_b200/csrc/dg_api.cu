@@ -809,16 +809,28 @@ static cudaError_t launch_quantize_int8(const QuantArgs& p, cudaStream_t st) {
 }
 
 // Elements a lane of the gate kernels holds: the smallest power of two that covers E.
-template <typename T>
-static cudaError_t launch_gate(const GateArgs& p, cudaStream_t st) {
+template <typename T, int V>
+static cudaError_t launch_gate_v(GateArgs& p, cudaStream_t st) {
+  const int span = p.gsize / V;
+  p.span_log2 = -1;
+  if (p.gsize % V == 0 && (span & (span - 1)) == 0)
+    for (p.span_log2 = 0; (1 << p.span_log2) < span;) ++p.span_log2;
   const long long blocks = (static_cast<long long>(p.T) + kGateWarps - 1) / kGateWarps;
   constexpr int th = 32 * kGateWarps;
-  if (p.E <= 32) return launch_plain(moe_gate_kernel<T, 1>, blocks, th, st, p);
-  if (p.E <= 64) return launch_plain(moe_gate_kernel<T, 2>, blocks, th, st, p);
-  if (p.E <= 128) return launch_plain(moe_gate_kernel<T, 4>, blocks, th, st, p);
-  if (p.E <= 256) return launch_plain(moe_gate_kernel<T, 8>, blocks, th, st, p);
-  if (p.E <= 512) return launch_plain(moe_gate_kernel<T, 16>, blocks, th, st, p);
-  return launch_plain(moe_gate_kernel<T, 32>, blocks, th, st, p);
+  if (p.sigmoid)
+    return p.bias ? launch_plain(moe_gate_kernel<T, V, true, true>, blocks, th, st, p)
+                  : launch_plain(moe_gate_kernel<T, V, true, false>, blocks, th, st, p);
+  return p.bias ? launch_plain(moe_gate_kernel<T, V, false, true>, blocks, th, st, p)
+                : launch_plain(moe_gate_kernel<T, V, false, false>, blocks, th, st, p);
+}
+template <typename T>
+static cudaError_t launch_gate(GateArgs& p, cudaStream_t st) {
+  if (p.E <= 32) return launch_gate_v<T, 1>(p, st);
+  if (p.E <= 64) return launch_gate_v<T, 2>(p, st);
+  if (p.E <= 128) return launch_gate_v<T, 4>(p, st);
+  if (p.E <= 256) return launch_gate_v<T, 8>(p, st);
+  if (p.E <= 512) return launch_gate_v<T, 16>(p, st);
+  return launch_gate_v<T, 32>(p, st);
 }
 template <typename T>
 static cudaError_t launch_gate_backward(const GateBackwardArgs& p, cudaStream_t st) {
@@ -1431,6 +1443,7 @@ int dg_moe_gate(const void* logits, int logits_dtype, const float* bias, int T, 
   p.n_group = topk_group == n_group ? 1 : n_group;  // every group stays: no group is looked at
   p.topk_group = topk_group;
   p.group_top = group_top;
+  p.gsize = gsize;
   p.sigmoid = score_func == DG_SCORE_SIGMOID;
   p.renorm = renormalize;
   p.scale = scale;

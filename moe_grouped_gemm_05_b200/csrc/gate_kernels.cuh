@@ -36,6 +36,8 @@ struct GateArgs {
   const float* bias;    // [E] or nullptr
   int T, E, topk;
   int n_group, topk_group, group_top;
+  int gsize;            // experts of a group
+  int span_log2;        // a group is 2^span_log2 whole lanes, or -1
   int sigmoid, renorm;
   float scale;
   int32_t* ids;         // [T][topk]
@@ -171,17 +173,11 @@ __device__ __forceinline__ float gate_at(const __nv_bfloat16* row, int e) { retu
 
 // ---------------------------------------------------------------- warp reductions
 
-// A float's bits as an unsigned key in the same order (no NaN; -0 and +0 differ).
-__device__ __forceinline__ uint32_t ordered_key(float x) {
-  const uint32_t b = __float_as_uint(x);
-  return b ^ (static_cast<uint32_t>(static_cast<int32_t>(b) >> 31) | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu));
-}
-
+// Largest of the warp's values (no NaN among them).
 __device__ __forceinline__ float warp_max(float x) {
-  return key_value(__reduce_max_sync(0xffffffffu, ordered_key(x)));
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+  return r;
 }
 template <typename R>
 __device__ __forceinline__ R warp_sum(R x) {
@@ -189,6 +185,27 @@ __device__ __forceinline__ R warp_sum(R x) {
   for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
 }
+
+// max(a, |b|), a NaN's place taken by NaN.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
+// 2^x and 1/x by the approximate instructions, each within one unit in the
+// last place of 2^-22 or better, subnormals taken as zero.
+__device__ __forceinline__ float fast_exp2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float fast_rcp(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.4426950408889634f;
 
 // The two largest of {a1 >= a2} and {b1 >= b2}, in a1 >= a2.
 template <typename R>
@@ -207,10 +224,13 @@ __device__ __forceinline__ R group_score(R a1, R a2, int group_top) {
 }
 
 // Scores of all groups for any group size: lane g gets group g's (-inf behind
-// the last).  v: the lane's V values, -inf where an expert cannot be chosen.
+// the last) and the size of the terms it is the sum of.  v: the lane's V
+// values, -inf where an expert cannot be chosen.
 template <typename R, int V>
-__device__ __forceinline__ R group_scores_any(const R (&v)[V], int lane, int n_group, int gsize, int group_top) {
+__device__ __forceinline__ R group_scores_any(const R (&v)[V], int lane, int n_group, int gsize, int group_top,
+                                              R& size) {
   R mine = -INFINITY;
+  size = 0;
   for (int g = 0; g < n_group; ++g) {
     R a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
@@ -223,7 +243,10 @@ __device__ __forceinline__ R group_scores_any(const R (&v)[V], int lane, int n_g
       const R b1 = __shfl_xor_sync(0xffffffffu, a1, o), b2 = __shfl_xor_sync(0xffffffffu, a2, o);
       merge_top2(a1, a2, b1, b2);
     }
-    if (lane == g) mine = group_score(a1, a2, group_top);
+    if (lane == g) {
+      mine = group_score(a1, a2, group_top);
+      size = (a1 == -INFINITY ? 0 : a1 < 0 ? -a1 : a1) + (a2 == -INFINITY ? 0 : a2 < 0 ? -a2 : a2);
+    }
   }
   return mine;
 }
@@ -264,8 +287,9 @@ __device__ __noinline__ int gate_choose64(const GateArgs& p, const LT* row, int 
     k[i] = p.bias || dead ? c[i] : k[i];  // without a bias the experts go by their logits
   }
   if (p.n_group > 1) {
-    const int gsize = p.E / p.n_group;
-    const double mine = group_scores_any<double, V>(c, lane, p.n_group, gsize, p.group_top);
+    const int gsize = p.gsize;
+    double size;
+    const double mine = group_scores_any<double, V>(c, lane, p.n_group, gsize, p.group_top, size);
     int rank = 0;
     for (int j = 0; j < p.n_group; ++j) {
       const double o = __shfl_sync(0xffffffffu, mine, j);
@@ -306,38 +330,74 @@ __device__ __noinline__ int gate_choose64(const GateArgs& p, const LT* row, int 
 
 // ---------------------------------------------------------------- forward
 
+// Sum of exp(l - top) over the row in 64 bits (every lane returns it).
+template <typename LT, int V>
+__device__ __noinline__ double gate_total64(const LT* row, int E, int lane, float top) {
+  double sum = 0.0;
+  for (int i = 0; i < V; ++i) {
+    const int e = lane + 32 * i;
+    if (e < E) sum += exp(static_cast<double>(gate_at(row, e)) - static_cast<double>(top));
+  }
+  return warp_sum(sum);
+}
+
+// c of expert e in 64 bits; total64 from gate_total64 (softmax only).
+template <typename LT>
+__device__ __noinline__ double gate_score64(const GateArgs& p, const LT* row, int e, float top, double total64) {
+  const double x = gate_at(row, e);
+  const double s = p.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - static_cast<double>(top)) / total64;
+  return p.bias ? s + static_cast<double>(__ldg(p.bias + e)) : s;
+}
+
 // One warp a token.
 //
-// Error of a 32-bit score (u = 2^-24, __expf within 2 + 1.173|x| units of 2u):
-//   sigmoid  s(1-s)(2 + 1.173|l|) 2u <= (0.5 + 0.27) 2u, with the sum and the
-//            division at most 4u = 2^-22; c adds |c| u, |c| <= 1 + |bias|.
-//   softmax  p (2^-18 + 2^-21) from the sum over at most 1024 terms and the
-//            quotient, 0.61 * 2u from the exponent's argument: <= p 2^-17 + 2^-23.
-// Two values closer than `near` (both errors, rounded up) are not told apart;
-// a sum of two has twice the error.
-template <typename LT, int V>
-__global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const GateArgs p) {
+// Error of a 32-bit score (u = 2^-24).  ex2.approx and rcp.approx are within
+// 2^-22 = 4u relative; the argument x log2(e) of ex2 is off by 2u |x| log2(e)
+// (the constant's rounding and the product's), which is 2u |x| relative in the
+// exponential.
+//   sigmoid  s(1-s)(4 + 2|l|) u <= (1 + 0.45) u, the sum u, the quotient 4u:
+//            below 7u.
+//   softmax  p |x| 2u <= 0.74u and 4u p from the exponential; from the sum (at
+//            most 1024 terms, in 64 bits (2 + 2 * 6.94) u of their own and 37 u
+//            of additions) and the quotient 60u p: <= p 2^-17 + u.
+// c adds |c| u.  Two values closer than both errors together (`near`, and 2u
+// of their sizes) are not told apart; a sum of two has both terms' errors.
+//
+// The choice.  The topk-th largest of the lanes' best values is a lower bound
+// of the topk-th best value of the row, since so many values reach it, and few
+// values do (for 256 experts, topk 8: about ten).  Those (and the ones closer
+// below it than `near`) are put together in shared memory, one a lane, and each
+// lane counts the ones before its own.  That takes the place of topk rounds of
+// finding and removing the best (which serve the rows with more than 32).
+template <typename LT, int V, bool SIGMOID, bool BIAS>
+__global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_constant__ GateArgs p) {
+  __shared__ float2 cand[kGateWarps][32 * V];  // value, expert
+  __shared__ int count[kGateWarps];
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
-  const int t = blockIdx.x * kGateWarps + (threadIdx.x >> 5);
+  const int warp = threadIdx.x >> 5;
+  const int t = blockIdx.x * kGateWarps + warp;
   if (t >= p.T) return;
   const LT* row = static_cast<const LT*>(p.logits) + static_cast<size_t>(t) * p.E;
-  int32_t* ids = p.ids + static_cast<size_t>(t) * p.topk;
-  float* weights = p.weights + static_cast<size_t>(t) * p.topk;
+  float2* list = cand[warp];
 
-  float l[V];
-  gate_load_row<V>(row, p.E, lane, -INFINITY, l);
-  bool bad = false;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    bad |= !(l[i] < INFINITY);  // +inf or NaN
-    l[i] += 0.0f;               // -0 becomes +0, so that equal logits have equal keys
-  }
   const bool sums = p.n_group > 1 && p.group_top > 1;
-  const bool scored = p.bias != nullptr || sums;
+  const bool scored = BIAS || sums;
+  const bool full = p.E == 32 * V;                  // every lane holds V experts
+  const int live = full ? V : min(V, max(0, p.E - lane * V));
+  float l[V], c[V];
+  gate_load_row<V>(row, p.E, lane, -FLT_MAX, l);
+  float big = 0.0f;  // the largest magnitude: below infinity when nothing is masked or bad
+#pragma unroll
+  for (int i = 0; i < V; ++i) big = max_abs_nan(big, l[i]);
+  if (BIAS) {
+    gate_load_row<V>(p.bias, p.E, lane, 0.0f, c);
+#pragma unroll
+    for (int i = 0; i < V; ++i) big = max_abs_nan(big, c[i]);
+  }
   float top = 0.0f, total = 1.0f;
-  if (!p.sigmoid && (scored || !p.renorm)) {
+  if (!SIGMOID && (scored || !p.renorm)) {
     float m = l[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
@@ -345,135 +405,241 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const GateArg
     if (top == -INFINITY) top = 0.0f;
     float sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < V; ++i) sum += expf(l[i] - top);
+    for (int i = 0; i < V; ++i) sum += i < live ? expf(l[i] - top) : 0.0f;
     total = warp_sum(sum);
   }
-  // c: what groups are ranked by; key: what experts are ranked by (0: cannot be chosen)
-  float c[V];
-  uint32_t key[V];
   float near = 0.0f;
   if (scored) {
-    float big = 0.0f;
-    float b[V];
-    if (p.bias) gate_load_row<V>(p.bias, p.E, lane, 0.0f, b);
+    const float inv = SIGMOID ? 1.0f : fast_rcp(total);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const float s = p.sigmoid ? __frcp_rn(1.0f + __expf(-l[i])) : __fdividef(__expf(l[i] - top), total);
-      c[i] = s;
-      if (p.bias) {
-        bad |= !(b[i] < INFINITY);
-        c[i] = s + b[i] + 0.0f;
-        if (b[i] > -INFINITY) big = fmaxf(big, fabsf(b[i]));
-        if (l[i] == -INFINITY) c[i] = -INFINITY;
-      } else if (l[i] == -INFINITY) {
-        c[i] = -INFINITY;
-      }
-      const float by = p.bias ? c[i] : l[i];
-      key[i] = by == -INFINITY ? 0u : ordered_key(by);
+      const float s = SIGMOID ? fast_rcp(1.0f + fast_exp2(-kLog2e * l[i])) : fast_exp2(kLog2e * (l[i] - top)) * inv;
+      c[i] = BIAS ? s + c[i] : s;
     }
-    near = 0x1p-21f + (p.sigmoid ? 0.0f : __fdividef(0x1p-16f, total));
-    if (p.bias) near += 0x1p-22f * (1.0f + warp_max(big));
+    near = 0x1p-20f + (SIGMOID ? 0.0f : 0x1p-16f * inv);
   } else {
 #pragma unroll
+    for (int i = 0; i < V; ++i) c[i] = l[i];
+  }
+  // masks, and rows that are not numbers
+  if (__any_sync(0xffffffffu, !(big < INFINITY))) {
+    bool bad = false;
+#pragma unroll
     for (int i = 0; i < V; ++i) {
-      c[i] = l[i];
-      key[i] = l[i] == -INFINITY ? 0u : ordered_key(l[i]);
+      const int e = lane * V + i;
+      const float b = BIAS && i < live ? __ldg(p.bias + e) : 0.0f;
+      bad |= i < live && (!(l[i] < INFINITY) || !(b < INFINITY));
+      if (l[i] == -INFINITY || b == -INFINITY) c[i] = -INFINITY;
+    }
+    if (__any_sync(0xffffffffu, bad)) {
+      // NaN or +inf among the logits or the bias: the token is not routed
+      if (lane == 0) atomicOr(&g_dg_error, 0x20);
+      if (lane < p.topk) {
+        p.ids[static_cast<size_t>(t) * p.topk + lane] = -1;
+        p.weights[static_cast<size_t>(t) * p.topk + lane] = 0.0f;
+      }
+      return;
     }
   }
-  if (__any_sync(0xffffffffu, bad)) {
-    // NaN or +inf among the logits or the bias: the token is not routed
-    if (lane == 0) atomicOr(&g_dg_error, 0x20);
-    if (lane < p.topk) {
-      ids[lane] = -1;
-      weights[lane] = 0.0f;
-    }
-    return;
+  if (!full) {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i >= live) c[i] = -INFINITY;
   }
 
-  bool unsure = false;
+  bool unsure = false;  // the row needs the choice in 64 bits (all lanes agree)
   if (p.n_group > 1) {
-    const int gsize = p.E / p.n_group;
-    const int span = gsize / V;  // lanes of a group, where its experts are whole lanes of a power of two
-    const bool whole = gsize % V == 0 && (span & (span - 1)) == 0;
-    float mine;
+    const bool whole = p.span_log2 >= 0;
+    const int span = whole ? 1 << p.span_log2 : 1;  // lanes that hold the same group
+    float mine, size;
     int at;  // the group whose score this lane holds
+    float a1 = c[0], a2 = -INFINITY;
     if (whole) {
-      float a1 = c[0], a2 = -INFINITY;
 #pragma unroll
-      for (int i = 1; i < V; ++i) merge_top2(a1, a2, c[i], -INFINITY);
+      for (int i = 1; i < V; ++i) {
+        a2 = fmaxf(a2, fminf(a1, c[i]));
+        a1 = fmaxf(a1, c[i]);
+      }
       for (int o = 1; o < span; o <<= 1) {
         const float b1 = __shfl_xor_sync(0xffffffffu, a1, o), b2 = __shfl_xor_sync(0xffffffffu, a2, o);
-        merge_top2(a1, a2, b1, b2);
+        a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
+        a1 = fmaxf(a1, b1);
       }
       mine = group_score(a1, a2, p.group_top);
-      at = lane / span;
+      size = (a1 > -INFINITY ? fabsf(a1) : 0.0f) + (a2 > -INFINITY ? fabsf(a2) : 0.0f);
+      at = lane >> p.span_log2;
     } else {
-      mine = group_scores_any<float, V>(c, lane, p.n_group, gsize, p.group_top);
+      mine = group_scores_any<float, V>(c, lane, p.n_group, p.gsize, p.group_top, size);
       at = lane;
     }
-    // near for groups: twice an expert's, and the rounding of the sum
-    const float gnear = scored ? (sums ? 2.0f * near + 0x1p-22f : near) : 0.0f;
-    int above = 0, sure_above = 0, maybe_above = 0;
-    for (int j = 0; j < p.n_group; ++j) {
-      const float o = __shfl_sync(0xffffffffu, mine, whole ? j * span : j);
-      above += o > mine || (o == mine && j < at);
-      sure_above += o > mine + gnear;
-      maybe_above += o >= mine - gnear && j != at;
-    }
-    const bool mine_kept = at < p.n_group && above < p.topk_group && mine > -INFINITY;
-    if (scored && at < p.n_group && mine > -INFINITY)
-      unsure = !(maybe_above < p.topk_group || sure_above >= p.topk_group);
-    if (whole) {
-      if (!mine_kept) {
-#pragma unroll
-        for (int i = 0; i < V; ++i) key[i] = 0u;
+    // a group's error: that of its terms and of their sum
+    const float gnear = scored ? 2.0f * near + 0x1p-21f * warp_max(size) : 0.0f;
+    // groups before this one (low half), and groups that it is not told apart from (high half); the
+    // lanes of a group share the comparisons
+    int seen = 0;
+    for (int j = lane & (span - 1); j - (lane & (span - 1)) < p.n_group; j += span) {
+      const float o = __shfl_sync(0xffffffffu, mine, (j * span) & 31);
+      if (j < p.n_group) {
+        seen += o > mine || (o == mine && j < at);
+        seen += j != at && fabsf(o - mine) <= gnear ? 0x10000 : 0;  // (-inf - -inf is NaN: not close)
       }
-    } else {
-      const uint32_t kept = __ballot_sync(0xffffffffu, mine_kept);
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (!((kept >> min(31, (lane * V + i) / gsize)) & 1)) key[i] = 0u;
     }
-    unsure = __any_sync(0xffffffffu, unsure);
-  }
-
-  // The best key of the warp, topk times; one more shows whether the last
-  // place was a close one.
-  int mine_id = -1;
-  if (!unsure) {
-    const int rounds = p.bias ? p.topk + 1 : p.topk;
-    float before = INFINITY;
-    int before_id = -1;
-    for (int j = 0; j < rounds; ++j) {
-      uint32_t best = key[0];
-#pragma unroll
-      for (int i = 1; i < V; ++i) best = max(best, key[i]);
-      const uint32_t all = __reduce_max_sync(0xffffffffu, best);
-      if (all == 0u) break;
-      const int src = __ffs(__ballot_sync(0xffffffffu, best == all)) - 1;
-      int at = 0;
-      if (lane == src) {
-        bool found = false;
+    for (int o = 1; o < span; o <<= 1) seen += __shfl_xor_sync(0xffffffffu, seen, o);
+    const bool some = at < p.n_group && mine > -INFINITY;  // a group, and one with an expert to choose
+    bool kept = some && (seen & 0xFFFF) < p.topk_group;
+    if (scored && __any_sync(0xffffffffu, some && seen >= 0x10000)) {
+      // is a kept group too close to one that is not?
+      int sure_above = 0, maybe_above = 0;
+      for (int j = 0; j < p.n_group; ++j) {
+        const float o = __shfl_sync(0xffffffffu, mine, j * span);
+        sure_above += o > mine + gnear;
+        maybe_above += j != at && o >= mine - gnear;
+      }
+      unsure = __any_sync(0xffffffffu, some && maybe_above >= p.topk_group && sure_above < p.topk_group);
+      if (unsure && whole) {
+        // The groups' scores in 64 bits, from the one or two experts that each
+        // is made of, if 32 bits tell those from the group's others.
+        const float last = p.group_top == 1 || a2 == -INFINITY ? a1 : a2;
+        const float lowest = last - near - 0x1p-22f * fabsf(last);
+        int n = 0, e1 = -1, e2 = -1;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (!found && key[i] == all) {
-            found = true;
-            key[i] = 0u;
-            at = lane * V + i;
+          if (c[i] >= lowest && c[i] > -INFINITY) {
+            e2 = e1;
+            e1 = lane * V + i;
+            ++n;
           }
+        for (int o = 1; o < span; o <<= 1) {
+          const int f1 = __shfl_xor_sync(0xffffffffu, e1, o), f2 = __shfl_xor_sync(0xffffffffu, e2, o);
+          n += __shfl_xor_sync(0xffffffffu, n, o);
+          // (right when there are two of them in all, and not used otherwise)
+          const int x1 = e1 >= 0 ? e1 : f1, x2 = e1 >= 0 ? (e2 >= 0 ? e2 : f1) : f2;
+          e1 = x1;
+          e2 = x2;
+        }
+        const int want = p.group_top == 1 || a2 == -INFINITY ? 1 : 2;
+        if (__all_sync(0xffffffffu, !some || n == want)) {
+          const double total64 = SIGMOID ? 1.0 : gate_total64<LT, V>(row, p.E, lane, top);
+          double exact = -INFINITY;
+          if (some) {
+            exact = gate_score64(p, row, e1, top, total64);
+            if (want == 2) exact += gate_score64(p, row, e2, top, total64);
+          }
+          __syncwarp();
+          int above = 0;
+          for (int j = 0; j < p.n_group; ++j) {
+            const double o = __shfl_sync(0xffffffffu, exact, j * span);
+            above += o > exact || (o == exact && j < at);
+          }
+          kept = some && above < p.topk_group;
+          unsure = false;
+        }
       }
-      at = __shfl_sync(0xffffffffu, at, src);
-      if (p.bias) {
-        const float v = key_value(all);
-        if (before - v <= near &&
-            !(gate_at(row, at) == gate_at(row, before_id) && __ldg(p.bias + at) == __ldg(p.bias + before_id))) {
+    }
+    if (whole) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = kept ? c[i] : -INFINITY;
+    } else {
+      const uint32_t all_kept = __ballot_sync(0xffffffffu, kept);
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+        if (!((all_kept >> min(31, (lane * V + i) / p.gsize)) & 1)) c[i] = -INFINITY;
+    }
+    if (!BIAS && sums) {  // the groups went by scores, their experts go by the logits
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = c[i] == -INFINITY ? c[i] : l[i];
+    }
+  }
+
+  int mine_id = -1;
+  if (!unsure) {
+    float best = c[0];
+#pragma unroll
+    for (int i = 1; i < V; ++i) best = fmaxf(best, c[i]);
+    if (lane == 0) count[warp] = 0;
+    float kth = -INFINITY;
+    for (int j = 0; j < p.topk; ++j) {
+      kth = warp_max(best);
+      best = best == kth ? -INFINITY : best;
+    }
+    // (-FLT_MAX where fewer lanes than topk have an expert: every one is in question)
+    const float bound = kth == -INFINITY ? -FLT_MAX : BIAS ? kth - near - 0x1p-22f * fabsf(kth) : kth;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) n += c[i] >= bound;
+    __syncwarp();
+    int pos = n > 0 ? atomicAdd(&count[warp], n) : 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (c[i] >= bound) list[pos++] = make_float2(c[i], __int_as_float(lane * V + i));
+    __syncwarp();
+    const int m = count[warp];
+    if (m <= 32) {
+      // the place of candidate `lane` (of lane % 16, from half of the others, where no more than 16 are)
+      const bool two = m <= 16;
+      const int own = two ? lane & 15 : lane;
+      const float2 x = own < m ? list[own] : make_float2(-INFINITY, 0.0f);
+      int rank = 0;
+      for (int j = two ? lane >> 4 : 0; j < m; j += two ? 2 : 1) {
+        const float2 o = list[j];
+        rank += o.x > x.x || (o.x == x.x && __float_as_int(o.y) < __float_as_int(x.y));
+      }
+      __syncwarp();
+      if (two) rank += __shfl_xor_sync(0xffffffffu, rank, 16);
+      if (lane < m) list[rank] = x;
+      __syncwarp();
+      float2 y = lane < m ? list[lane] : make_float2(-INFINITY, __int_as_float(-1));
+      if (BIAS) {
+        // neighbours in the order, down to the first behind the chosen ones
+        const float next = __shfl_down_sync(0xffffffffu, y.x, 1);
+        if (__any_sync(0xffffffffu, lane < p.topk && lane + 1 < m && y.x - next <= near + 0x1p-22f * fabsf(y.x))) {
+          const int e = __float_as_int(y.y);
+          const double total64 = SIGMOID ? 1.0 : gate_total64<LT, V>(row, p.E, lane, top);
+          const double z = lane < m ? gate_score64(p, row, e, top, total64) : -INFINITY;
+          __syncwarp();
+          rank = 0;
+          for (int j = 0; j < m; ++j) {
+            const double o = __shfl_sync(0xffffffffu, z, j);
+            const int oe = __shfl_sync(0xffffffffu, e, j);
+            rank += o > z || (o == z && oe < e);
+          }
+          if (lane < m) list[rank] = y;
+          __syncwarp();
+          if (lane < m) y = list[lane];
+        }
+      }
+      mine_id = lane < p.topk ? __float_as_int(y.y) : -1;
+    } else {
+      // more than 32 in question: the best of the warp, topk times; one more
+      // shows whether the last place was a close one
+      const int rounds = BIAS ? p.topk + 1 : p.topk;
+      float before = INFINITY;
+      for (int j = 0; j < rounds; ++j) {
+        float lead = c[0];
+#pragma unroll
+        for (int i = 1; i < V; ++i) lead = fmaxf(lead, c[i]);
+        const float all = warp_max(lead);
+        if (all == -INFINITY) break;
+        if (BIAS && before - all <= near + 0x1p-22f * fabsf(before)) {
           unsure = true;
           break;
         }
-        before = v;
-        before_id = at;
+        before = all;
+        const int src = __ffs(__ballot_sync(0xffffffffu, lead == all)) - 1;
+        int at = 0;
+        if (lane == src) {
+          bool found = false;
+#pragma unroll
+          for (int i = 0; i < V; ++i)
+            if (!found && c[i] == all) {
+              found = true;
+              c[i] = -INFINITY;
+              at = lane * V + i;
+            }
+        }
+        at = __shfl_sync(0xffffffffu, at, src);
+        if (lane == j && j < p.topk) mine_id = at;
       }
-      if (lane == j && j < p.topk) mine_id = at;
     }
   }
   if (unsure) mine_id = gate_choose64<LT, V>(p, row, lane);
@@ -485,18 +651,18 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const GateArg
     // s_j / sum s from the ratios to the largest: no under- or overflow however small the scores
     const float m = warp_max(x);
     float v;
-    if (p.sigmoid) v = x < 0.0f ? expf(x - fminf(m, 0.0f)) / (1.0f + expf(x)) : 1.0f / (1.0f + expf(-x));
+    if (SIGMOID) v = __fdiv_rn(expf(fminf(x, 0.0f) - fminf(m, 0.0f)), 1.0f + expf(-fabsf(x)));
     else v = expf(x - m);
-    if (!has) v = 0.0f;
-    w = v / warp_sum(v);
-  } else if (p.sigmoid) {
-    w = x < 0.0f ? expf(x) / (1.0f + expf(x)) : 1.0f / (1.0f + expf(-x));
+    v = has ? v : 0.0f;
+    w = __fdiv_rn(v, warp_sum(v));
+  } else if (SIGMOID) {
+    w = __fdiv_rn(expf(fminf(x, 0.0f)), 1.0f + expf(-fabsf(x)));
   } else {
-    w = expf(x - top) / total;
+    w = __fdiv_rn(expf(x - top), total);
   }
   if (lane < p.topk) {
-    ids[lane] = mine_id;
-    weights[lane] = has ? p.scale * w : 0.0f;
+    p.ids[static_cast<size_t>(t) * p.topk + lane] = mine_id;
+    p.weights[static_cast<size_t>(t) * p.topk + lane] = has ? p.scale * w : 0.0f;
   }
 }
 
@@ -507,12 +673,14 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const GateArg
 template <typename LT, int V>
 __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(const GateBackwardArgs p) {
   __shared__ __align__(16) float rows[kGateWarps][32 * V];
+  __shared__ int owner[kGateWarps][32 * V];
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
   const int t = blockIdx.x * kGateWarps + (threadIdx.x >> 5);
   if (t >= p.T) return;
   float* acc = rows[threadIdx.x >> 5];
+  int* slot = owner[threadIdx.x >> 5];
   const LT* row = static_cast<const LT*>(p.logits) + static_cast<size_t>(t) * p.E;
   LT* out = static_cast<LT*>(p.d_logits) + static_cast<size_t>(t) * p.E;
 
@@ -527,41 +695,53 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(cons
   float v = g;  // what the slot adds to its expert's place in `acc`
   if (!dense) {
     const float x = has ? gate_at(row, id) : -INFINITY;
-    // 1 - s, and s / sum s as in the forward pass
-    const float rest = x < 0.0f ? 1.0f / (1.0f + expf(x)) : expf(-x) / (1.0f + expf(-x));
+    // s = e^min(x,0) / (1 + e^-|x|) and 1 - s = e^-max(x,0) / (1 + e^-|x|)
+    const float tail = expf(-fabsf(x));
+    const float inv = __fdiv_rn(1.0f, 1.0f + tail);
+    const float rest = (x < 0.0f ? 1.0f : tail) * inv;
     if (p.renorm) {
       float m = warp_max(x);
       if (m == -INFINITY) m = 0.0f;
-      float r;
-      if (p.sigmoid) r = x < 0.0f ? expf(x - fminf(m, 0.0f)) / (1.0f + expf(x)) : 1.0f / (1.0f + expf(-x));
-      else r = expf(x - m);
-      if (!has) r = 0.0f;
+      // s / sum s as in the forward pass
+      float r = p.sigmoid ? expf(fminf(x, 0.0f) - fminf(m, 0.0f)) * inv : expf(x - m);
+      r = has ? r : 0.0f;
       const float sum = warp_sum(r);
-      r = sum > 0.0f ? r / sum : 0.0f;
+      r = sum > 0.0f ? __fdiv_rn(r, sum) : 0.0f;
       const float mean = warp_sum(r * g);
       v = p.scale * r * (p.sigmoid ? rest : 1.0f) * (g - mean);
     } else {
-      const float s = x < 0.0f ? expf(x) / (1.0f + expf(x)) : 1.0f / (1.0f + expf(-x));
-      v = p.scale * s * rest * g;
+      v = p.scale * ((x < 0.0f ? tail : 1.0f) * inv) * rest * g;
     }
   }
+  float o[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) acc[lane + 32 * i] = 0.0f;
+  for (int i = 0; i < V; ++i) o[i] = 0.0f;
+  gate_store_row<V>(acc, 32 * V, lane, o);
   __syncwarp();
-  // an expert named twice in a row takes both slots' share, in slot order
-  const uint32_t same = __match_any_sync(0xffffffffu, has ? id : -1 - lane);
-  if (__all_sync(0xffffffffu, (same & (same - 1)) == 0u)) {
-    if (has) acc[id] = v;
-  } else {
+  if (has) {
+    acc[id] = v;
+    slot[id] = lane;
+  }
+  __syncwarp();
+  if (__any_sync(0xffffffffu, has && slot[id] != lane)) {
+    // an expert named twice in a row takes both slots' share, in slot order
+    if (has) acc[id] = 0.0f;
+    __syncwarp();
     for (int j = 0; j < p.topk; ++j) {
       if (lane == j && has) acc[id] += v;
       __syncwarp();
     }
   }
-  __syncwarp();
-  float o[V];
+  if constexpr (V >= 4) {
 #pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = acc[lane * V + i];
+    for (int i = 0; i < V / 4; ++i) {
+      const float4 q = reinterpret_cast<const float4*>(acc + lane * V)[i];
+      o[4 * i] = q.x, o[4 * i + 1] = q.y, o[4 * i + 2] = q.z, o[4 * i + 3] = q.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) o[i] = acc[lane * V + i];
+  }
   if (dense && __any_sync(0xffffffffu, has)) {
     float l[V];
     gate_load_row<V>(row, p.E, lane, -INFINITY, l);
