@@ -402,20 +402,26 @@ def moe_unpermute_combine(d_perm: torch.Tensor, row_of: torch.Tensor, weights=No
     return out
 
 
-def _launch_stream(t: torch.Tensor) -> int:
-    """The current stream of t's device, which must be the current device: the library launches there."""
-    dev = t.get_device()
-    if dev != torch.cuda.current_device():
-        raise ValueError(f"operands are on {t.device} but the current device is cuda:{torch.cuda.current_device()}")
-    return torch.cuda.current_stream(dev).cuda_stream
+# The current device and the current stream's handle, without the objects that torch.cuda wraps around them
+# (1.6 us of an 8 us call).
+_current_device = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda dev: torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _operand(t, dtypes, shape, name: str, device) -> int:
-    """Checks one operand (dtype, shape, contiguity, device) and returns its address."""
+def _launch_stream(dev: int) -> int:
+    """The current stream of device `dev`, which must be the current device: the library launches there."""
+    if dev != _current_device():
+        raise ValueError(f"operands are on cuda:{dev} but the current device is cuda:{_current_device()}")
+    return _current_stream(dev)
+
+
+def _operand(t, dtypes, shape, name: str, dev: int) -> int:
+    """Checks one operand (dtype, shape, contiguity, device number) and returns its address."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on {device}, got shape "
+    if t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on cuda:{dev}, got shape "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
@@ -447,16 +453,16 @@ def moe_gate(logits, topk: int, bias=None, *, score: str = "softmax", n_group: i
         raise ValueError(f"unknown score {score!r}: softmax or sigmoid")
     _cuda_matrix(logits, _BF16_F32, "logits")
     T, E = logits.shape
-    dev = logits.device
+    dev = logits.get_device()
     if ids is None:
-        ids = torch.empty((T, max(0, topk)), dtype=torch.int32, device=dev)
+        ids = torch.empty((T, max(0, topk)), dtype=torch.int32, device=logits.device)
     if weights is None:
-        weights = torch.empty((T, max(0, topk)), dtype=torch.float32, device=dev)
+        weights = torch.empty((T, max(0, topk)), dtype=torch.float32, device=logits.device)
     _check(load().dg_moe_gate(logits.data_ptr(), _FLOAT_CODES[logits.dtype],
                               _operand(bias, _F32T, (E,), "bias", dev) if bias is not None else None, T, E, topk,
                               _SCORES[score], n_group, topk_group, group_top, 1 if renormalize else 0, scale,
                               _operand(ids, _I32T, (T, topk), "ids", dev),
-                              _operand(weights, _F32T, (T, topk), "weights", dev), _launch_stream(logits)))
+                              _operand(weights, _F32T, (T, topk), "weights", dev), _launch_stream(dev)))
     return ids, weights
 
 
@@ -473,7 +479,7 @@ def moe_gate_backward(logits, topk_ids, d_weights, *, score: str = "softmax", re
     _cuda_matrix(topk_ids, _I32T, "topk_ids")
     T, E = logits.shape
     topk = topk_ids.shape[1]
-    dev = logits.device
+    dev = logits.get_device()
     if d_logits is None:
         d_logits = torch.empty_like(logits)
     _check(load().dg_moe_gate_backward(logits.data_ptr(), _FLOAT_CODES[logits.dtype],
@@ -481,7 +487,7 @@ def moe_gate_backward(logits, topk_ids, d_weights, *, score: str = "softmax", re
                                        _operand(d_weights, _F32T, (T, topk), "d_weights", dev), T, E, topk,
                                        _SCORES[score], 1 if renormalize else 0, scale,
                                        _operand(d_logits, (logits.dtype,), (T, E), "d_logits", dev),
-                                       _launch_stream(logits)))
+                                       _launch_stream(dev)))
     return d_logits
 
 
@@ -492,14 +498,14 @@ def quantize_int8_per_token(x, q=None, scale=None):
     """
     _cuda_matrix(x, _BF16_F32, "x", max(1, x.dim()))
     lead, K = x.shape[:-1], x.shape[-1]
-    dev = x.device
+    dev = x.get_device()
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.int8, device=dev)
+        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
     if scale is None:
-        scale = torch.empty(lead, dtype=torch.float32, device=dev)
+        scale = torch.empty(lead, dtype=torch.float32, device=x.device)
     qp, sp = _operand(q, _INT8, x.shape, "q", dev), _operand(scale, _F32T, lead, "scale", dev)
     _check(load().dg_quantize_int8_per_token(x.data_ptr(), _FLOAT_CODES[x.dtype], qp, sp, lead.numel(), K,
-                                             _launch_stream(x)))
+                                             _launch_stream(dev)))
     return q, scale
 
 
@@ -521,14 +527,14 @@ def moe_quantize_permute_int8(topk_ids, num_experts: int, x, out=None):
     cap = lib.dg_moe_permute_capacity(T, topk, num_experts)
     if cap < 0:
         _check(cap)
-    dev = x.device
+    dev = x.get_device()
     if out is None:
         out = {
-            "a": torch.empty((cap, K), dtype=torch.int8, device=dev),
-            "sa": torch.empty((cap,), dtype=torch.float32, device=dev),
-            "m_indices": torch.empty((cap,), dtype=torch.int32, device=dev),
-            "src_of": torch.empty((cap,), dtype=torch.int32, device=dev),
-            "row_of": torch.empty((T, topk), dtype=torch.int32, device=dev),
+            "a": torch.empty((cap, K), dtype=torch.int8, device=x.device),
+            "sa": torch.empty((cap,), dtype=torch.float32, device=x.device),
+            "m_indices": torch.empty((cap,), dtype=torch.int32, device=x.device),
+            "src_of": torch.empty((cap,), dtype=torch.int32, device=x.device),
+            "row_of": torch.empty((T, topk), dtype=torch.int32, device=x.device),
         }
     else:
         for key in ("a", "sa", "m_indices", "src_of", "row_of"):
@@ -539,7 +545,7 @@ def moe_quantize_permute_int8(topk_ids, num_experts: int, x, out=None):
         _operand(out["a"], _INT8, (cap, K), "out['a']", dev), _operand(out["sa"], _F32T, (cap,), "out['sa']", dev),
         _operand(out["m_indices"], _I32T, (cap,), "out['m_indices']", dev),
         _operand(out["row_of"], _I32T, (T, topk), "out['row_of']", dev),
-        _operand(out["src_of"], _I32T, (cap,), "out['src_of']", dev), cap, _launch_stream(x)))
+        _operand(out["src_of"], _I32T, (cap,), "out['src_of']", dev), cap, _launch_stream(dev)))
     return out
 
 
@@ -552,15 +558,15 @@ def int8_gemm_nt(a, sa, b, sb, d=None, out_dtype=torch.bfloat16) -> torch.Tensor
     _cuda_matrix(a, _INT8, "a")
     M, K = a.shape
     N = b.shape[0]
-    dev = a.device
+    dev = a.get_device()
     if d is None:
         if out_dtype not in _BF16_F32:
             raise ValueError("out_dtype must be bfloat16 or float32")
-        d = torch.empty((M, N), dtype=out_dtype, device=dev)
+        d = torch.empty((M, N), dtype=out_dtype, device=a.device)
     _check(load().dg_int8_gemm_nt(a.data_ptr(), _operand(sa, _F32T, (M,), "sa", dev),
                                   _operand(b, _INT8, (N, K), "b", dev), _operand(sb, _F32T, (N,), "sb", dev),
                                   _operand(d, _BF16_F32, (M, N), "d", dev), M, N, K,
-                                  1 if d.dtype == torch.float32 else 0, _launch_stream(a)))
+                                  1 if d.dtype == torch.float32 else 0, _launch_stream(dev)))
     return d
 
 
@@ -571,13 +577,13 @@ def m_grouped_int8_gemm_nt_contiguous(a, sa, b, sb, m_indices, d=None) -> torch.
     _cuda_matrix(b, _INT8, "b", 3)
     M, K = a.shape
     G, N, _ = b.shape
-    dev = a.device
+    dev = a.get_device()
     if d is None:
-        d = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        d = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
     _check(load().dg_m_grouped_int8_gemm_nt_contiguous(
         a.data_ptr(), _operand(sa, _F32T, (M,), "sa", dev), _operand(b, _INT8, (G, N, K), "b", dev),
         _operand(sb, _F32T, (G, N), "sb", dev), _operand(d, _BF16T, (M, N), "d", dev),
-        _operand(m_indices, _I32T, (M,), "m_indices", dev), M, N, K, G, _launch_stream(a)))
+        _operand(m_indices, _I32T, (M,), "m_indices", dev), M, N, K, G, _launch_stream(dev)))
     return d
 
 
@@ -589,13 +595,13 @@ def m_grouped_int8_gemm_nt_masked(a, sa, b, sb, masked_m, d=None) -> torch.Tenso
     _cuda_matrix(b, _INT8, "b", 3)
     G, M_max, K = a.shape
     N = b.shape[1]
-    dev = a.device
+    dev = a.get_device()
     if d is None:
-        d = torch.empty((G, M_max, N), dtype=torch.bfloat16, device=dev)
+        d = torch.empty((G, M_max, N), dtype=torch.bfloat16, device=a.device)
     _check(load().dg_m_grouped_int8_gemm_nt_masked(
         a.data_ptr(), _operand(sa, _F32T, (G, M_max), "sa", dev), _operand(b, _INT8, (G, N, K), "b", dev),
         _operand(sb, _F32T, (G, N), "sb", dev), _operand(d, _BF16T, (G, M_max, N), "d", dev),
-        _operand(masked_m, _I32T, (G,), "masked_m", dev), G, M_max, N, K, _launch_stream(a)))
+        _operand(masked_m, _I32T, (G,), "masked_m", dev), G, M_max, N, K, _launch_stream(dev)))
     return d
 
 

@@ -111,7 +111,7 @@ def test_binding_refuses_before_the_library_is_called():
         dg.int8_gemm_nt(x, x, x, x)
     with pytest.raises(TypeError, match="int32"):
         dg.moe_quantize_permute_int8(x, 4, x)
-    cpu = torch.device("cpu")
+    cpu = -1      # the device number of CPU tensors
     assert dg._operand(x, (torch.float32,), (4, 16), "x", cpu) == x.data_ptr()
     with pytest.raises(TypeError):
         dg._operand(x, (torch.int8,), (4, 16), "x", cpu)
@@ -120,4 +120,4 @@ def test_binding_refuses_before_the_library_is_called():
     with pytest.raises(ValueError):
         dg._operand(x.t(), (torch.float32,), (16, 4), "x", cpu)
     with pytest.raises(ValueError):
-        dg._operand(x, (torch.float32,), (4, 16), "x", torch.device("cuda", 0))
+        dg._operand(x, (torch.float32,), (4, 16), "x", 0)
