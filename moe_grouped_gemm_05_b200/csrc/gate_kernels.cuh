@@ -224,13 +224,10 @@ __device__ __forceinline__ R group_score(R a1, R a2, int group_top) {
 }
 
 // Scores of all groups for any group size: lane g gets group g's (-inf behind
-// the last) and the size of the terms it is the sum of.  v: the lane's V
-// values, -inf where an expert cannot be chosen.
+// the last).  v: the lane's V values, -inf where an expert cannot be chosen.
 template <typename R, int V>
-__device__ __forceinline__ R group_scores_any(const R (&v)[V], int lane, int n_group, int gsize, int group_top,
-                                              R& size) {
+__device__ __forceinline__ R group_scores_any(const R (&v)[V], int lane, int n_group, int gsize, int group_top) {
   R mine = -INFINITY;
-  size = 0;
   for (int g = 0; g < n_group; ++g) {
     R a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
@@ -243,10 +240,7 @@ __device__ __forceinline__ R group_scores_any(const R (&v)[V], int lane, int n_g
       const R b1 = __shfl_xor_sync(0xffffffffu, a1, o), b2 = __shfl_xor_sync(0xffffffffu, a2, o);
       merge_top2(a1, a2, b1, b2);
     }
-    if (lane == g) {
-      mine = group_score(a1, a2, group_top);
-      size = (a1 == -INFINITY ? 0 : a1 < 0 ? -a1 : a1) + (a2 == -INFINITY ? 0 : a2 < 0 ? -a2 : a2);
-    }
+    if (lane == g) mine = group_score(a1, a2, group_top);
   }
   return mine;
 }
@@ -288,8 +282,7 @@ __device__ __noinline__ int gate_choose64(const GateArgs& p, const LT* row, int 
   }
   if (p.n_group > 1) {
     const int gsize = p.gsize;
-    double size;
-    const double mine = group_scores_any<double, V>(c, lane, p.n_group, gsize, p.group_top, size);
+    const double mine = group_scores_any<double, V>(c, lane, p.n_group, gsize, p.group_top);
     int rank = 0;
     for (int j = 0; j < p.n_group; ++j) {
       const double o = __shfl_sync(0xffffffffu, mine, j);
@@ -360,8 +353,9 @@ __device__ __noinline__ double gate_score64(const GateArgs& p, const LT* row, in
 //   softmax  p |x| 2u <= 0.74u and 4u p from the exponential; from the sum (at
 //            most 1024 terms, in 64 bits (2 + 2 * 6.94) u of their own and 37 u
 //            of additions) and the quotient 60u p: <= p 2^-17 + u.
-// c adds |c| u.  Two values closer than both errors together (`near`, and 2u
-// of their sizes) are not told apart; a sum of two has both terms' errors.
+// c = s + b adds |c| u <= (1 + B) u, B the largest |b|.  Two values closer than
+// both errors together (`near`) are not told apart; a sum of two has both
+// terms' errors and its own rounding, 2 (1 + B) u.
 //
 // The choice.  The topk-th largest of the lanes' best values is a lower bound
 // of the topk-th best value of the row, since so many values reach it, and few
@@ -377,24 +371,23 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
   const int warp = threadIdx.x >> 5;
+  float2* list = cand[warp];
   const int t = blockIdx.x * kGateWarps + warp;
   if (t >= p.T) return;
   const LT* row = static_cast<const LT*>(p.logits) + static_cast<size_t>(t) * p.E;
-  float2* list = cand[warp];
 
   const bool sums = p.n_group > 1 && p.group_top > 1;
   const bool scored = BIAS || sums;
-  const bool full = p.E == 32 * V;                  // every lane holds V experts
+  const bool full = p.E == 32 * V;  // every lane holds V experts
   const int live = full ? V : min(V, max(0, p.E - lane * V));
   float l[V], c[V];
   gate_load_row<V>(row, p.E, lane, -FLT_MAX, l);
-  float big = 0.0f;  // the largest magnitude: below infinity when nothing is masked or bad
+  if (BIAS) gate_load_row<V>(p.bias, p.E, lane, 0.0f, c);
+  float big = 0.0f, largest = 0.0f;  // the largest |logit| and |bias|: below infinity when nothing is masked or bad
 #pragma unroll
-  for (int i = 0; i < V; ++i) big = max_abs_nan(big, l[i]);
-  if (BIAS) {
-    gate_load_row<V>(p.bias, p.E, lane, 0.0f, c);
-#pragma unroll
-    for (int i = 0; i < V; ++i) big = max_abs_nan(big, c[i]);
+  for (int i = 0; i < V; ++i) {
+    big = max_abs_nan(big, l[i]);
+    if (BIAS) largest = max_abs_nan(largest, c[i]);
   }
   float top = 0.0f, total = 1.0f;
   if (!SIGMOID && (scored || !p.renorm)) {
@@ -422,14 +415,18 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
     for (int i = 0; i < V; ++i) c[i] = l[i];
   }
   // masks, and rows that are not numbers
-  if (__any_sync(0xffffffffu, !(big < INFINITY))) {
+  if (__any_sync(0xffffffffu, !(big < INFINITY) || !(largest < INFINITY))) {
     bool bad = false;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = lane * V + i;
-      const float b = BIAS && i < live ? __ldg(p.bias + e) : 0.0f;
-      bad |= i < live && (!(l[i] < INFINITY) || !(b < INFINITY));
-      if (l[i] == -INFINITY || b == -INFINITY) c[i] = -INFINITY;
+      bad |= i < live && !(l[i] < INFINITY);
+      if (l[i] == -INFINITY) c[i] = -INFINITY;
+      if (BIAS) {
+        const float b = i < live ? __ldg(p.bias + lane * V + i) : 0.0f;
+        bad |= !(b < INFINITY);
+        if (b == -INFINITY) c[i] = -INFINITY;
+        largest = fmaxf(i == 0 ? 0.0f : largest, b > -INFINITY ? fabsf(b) : 0.0f);
+      }
     }
     if (__any_sync(0xffffffffu, bad)) {
       // NaN or +inf among the logits or the bias: the token is not routed
@@ -441,6 +438,10 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       return;
     }
   }
+  if (BIAS) {
+    largest = warp_max(largest);
+    near += 0x1p-23f * (1.0f + largest);
+  }
   if (!full) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
@@ -451,8 +452,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
   if (p.n_group > 1) {
     const bool whole = p.span_log2 >= 0;
     const int span = whole ? 1 << p.span_log2 : 1;  // lanes that hold the same group
-    float mine, size;
-    int at;  // the group whose score this lane holds
+    float mine;
     float a1 = c[0], a2 = -INFINITY;
     if (whole) {
 #pragma unroll
@@ -466,41 +466,36 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
         a1 = fmaxf(a1, b1);
       }
       mine = group_score(a1, a2, p.group_top);
-      size = (a1 > -INFINITY ? fabsf(a1) : 0.0f) + (a2 > -INFINITY ? fabsf(a2) : 0.0f);
-      at = lane >> p.span_log2;
     } else {
-      mine = group_scores_any<float, V>(c, lane, p.n_group, p.gsize, p.group_top, size);
-      at = lane;
+      mine = group_scores_any<float, V>(c, lane, p.n_group, p.gsize, p.group_top);
     }
-    // a group's error: that of its terms and of their sum
-    const float gnear = scored ? 2.0f * near + 0x1p-21f * warp_max(size) : 0.0f;
-    // groups before this one (low half), and groups that it is not told apart from (high half); the
-    // lanes of a group share the comparisons
-    int seen = 0;
-    for (int j = lane & (span - 1); j - (lane & (span - 1)) < p.n_group; j += span) {
-      const float o = __shfl_sync(0xffffffffu, mine, (j * span) & 31);
-      if (j < p.n_group) {
-        seen += o > mine || (o == mine && j < at);
-        seen += j != at && fabsf(o - mine) <= gnear ? 0x10000 : 0;  // (-inf - -inf is NaN: not close)
-      }
+    // lanes behind the last group have -inf, as groups without an expert to choose
+    const float gnear = scored ? 2.0f * near + 0x1p-21f * (1.0f + largest) : 0.0f;
+    // the topk_group-th best score (equal ones once), and the best below it
+    float rest = mine, kth = -INFINITY;
+    for (int j = 0; j < p.topk_group; ++j) {
+      kth = warp_max(rest);
+      rest = rest == kth ? -INFINITY : rest;
     }
-    for (int o = 1; o < span; o <<= 1) seen += __shfl_xor_sync(0xffffffffu, seen, o);
-    const bool some = at < p.n_group && mine > -INFINITY;  // a group, and one with an expert to choose
-    bool kept = some && (seen & 0xFFFF) < p.topk_group;
-    if (scored && __any_sync(0xffffffffu, some && seen >= 0x10000)) {
-      // is a kept group too close to one that is not?
-      int sure_above = 0, maybe_above = 0;
+    bool kept = mine >= kth && mine > -INFINITY;
+    const bool close = scored && kth - warp_max(rest) <= gnear;  // (-inf - -inf is NaN: not close)
+    if (close || __popc(__ballot_sync(0xffffffffu, kept)) > p.topk_group * span) {
+      // a close call or equal scores: rank the groups one by one
+      const int at = whole ? lane >> p.span_log2 : lane;
+      const bool some = mine > -INFINITY;
+      int above = 0, sure_above = 0, maybe_above = 0;
       for (int j = 0; j < p.n_group; ++j) {
         const float o = __shfl_sync(0xffffffffu, mine, j * span);
+        above += o > mine || (o == mine && j < at);
         sure_above += o > mine + gnear;
         maybe_above += j != at && o >= mine - gnear;
       }
-      unsure = __any_sync(0xffffffffu, some && maybe_above >= p.topk_group && sure_above < p.topk_group);
+      kept = some && above < p.topk_group;
+      unsure = scored && __any_sync(0xffffffffu, some && maybe_above >= p.topk_group && sure_above < p.topk_group);
       if (unsure && whole) {
         // The groups' scores in 64 bits, from the one or two experts that each
         // is made of, if 32 bits tell those from the group's others.
-        const float last = p.group_top == 1 || a2 == -INFINITY ? a1 : a2;
-        const float lowest = last - near - 0x1p-22f * fabsf(last);
+        const float lowest = (p.group_top == 1 || a2 == -INFINITY ? a1 : a2) - near;
         int n = 0, e1 = -1, e2 = -1;
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -526,7 +521,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
             if (want == 2) exact += gate_score64(p, row, e2, top, total64);
           }
           __syncwarp();
-          int above = 0;
+          above = 0;
           for (int j = 0; j < p.n_group; ++j) {
             const double o = __shfl_sync(0xffffffffu, exact, j * span);
             above += o > exact || (o == exact && j < at);
@@ -563,7 +558,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       best = best == kth ? -INFINITY : best;
     }
     // (-FLT_MAX where fewer lanes than topk have an expert: every one is in question)
-    const float bound = kth == -INFINITY ? -FLT_MAX : BIAS ? kth - near - 0x1p-22f * fabsf(kth) : kth;
+    const float bound = kth == -INFINITY ? -FLT_MAX : BIAS ? kth - near : kth;
     int n = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) n += c[i] >= bound;
@@ -592,7 +587,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       if (BIAS) {
         // neighbours in the order, down to the first behind the chosen ones
         const float next = __shfl_down_sync(0xffffffffu, y.x, 1);
-        if (__any_sync(0xffffffffu, lane < p.topk && lane + 1 < m && y.x - next <= near + 0x1p-22f * fabsf(y.x))) {
+        if (__any_sync(0xffffffffu, lane < p.topk && lane + 1 < m && y.x - next <= near)) {
           const int e = __float_as_int(y.y);
           const double total64 = SIGMOID ? 1.0 : gate_total64<LT, V>(row, p.E, lane, top);
           const double z = lane < m ? gate_score64(p, row, e, top, total64) : -INFINITY;
@@ -620,7 +615,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
         for (int i = 1; i < V; ++i) lead = fmaxf(lead, c[i]);
         const float all = warp_max(lead);
         if (all == -INFINITY) break;
-        if (BIAS && before - all <= near + 0x1p-22f * fabsf(before)) {
+        if (BIAS && before - all <= near) {
           unsure = true;
           break;
         }
@@ -648,11 +643,12 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
   const float x = has ? gate_at(row, mine_id) : -INFINITY;
   float w;
   if (p.renorm) {
-    // s_j / sum s from the ratios to the largest: no under- or overflow however small the scores
+    // s_j / sum s; from the ratios to the largest, where the scores might underflow
     const float m = warp_max(x);
     float v;
-    if (SIGMOID) v = __fdiv_rn(expf(fminf(x, 0.0f) - fminf(m, 0.0f)), 1.0f + expf(-fabsf(x)));
-    else v = expf(x - m);
+    if (!SIGMOID) v = expf(x - m);
+    else if (m > -60.0f) v = __fdiv_rn(1.0f, 1.0f + expf(-x));
+    else v = __fdiv_rn(expf(x - m), 1.0f + expf(x));
     v = has ? v : 0.0f;
     w = __fdiv_rn(v, warp_sum(v));
   } else if (SIGMOID) {
