@@ -18,6 +18,9 @@
 //   sigmoid                 dl_j = scale s_j (1 - s_j) g_j
 //   softmax                 dl_e = scale p_e (G_e - sum_i p_i g_i),  G_e = g of e's slot or 0
 // (every form but the last is zero outside the chosen experts).
+//
+// A token belongs to a team of L lanes, half a warp or a whole one.  All lanes
+// of a warp take part in every shuffle and vote, whatever their team decides.
 #pragma once
 #include <cuda_bf16.h>
 #include <cfloat>
@@ -27,9 +30,10 @@
 
 namespace dg {
 
-constexpr int kGateMaxTopk = 32;    // lane j of the warp holds slot j
+constexpr int kGateMaxTopk = 32;    // lane j of the team holds slot j
 constexpr int kGateMaxGroups = 32;  // lane g holds group g
-constexpr int kGateWarps = 4;       // tokens of a block, one warp each
+constexpr int kGateWarps = 4;       // warps of a block
+constexpr int kGateList = 32;       // listed experts of a token that are ranked at once
 
 struct GateArgs {
   const void* logits;   // [T][E]
@@ -171,19 +175,61 @@ __device__ __forceinline__ void gate_store_row(__nv_bfloat16* row, int E, int la
 __device__ __forceinline__ float gate_at(const float* row, int e) { return __ldg(row + e); }
 __device__ __forceinline__ float gate_at(const __nv_bfloat16* row, int e) { return __bfloat162float(row[e]); }
 
-// ---------------------------------------------------------------- warp reductions
+// ---------------------------------------------------------------- reductions over a team
 
-// Largest of the warp's values (no NaN among them).
-__device__ __forceinline__ float warp_max(float x) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
-  return r;
-}
-template <typename R>
-__device__ __forceinline__ R warp_sum(R x) {
+// Largest of the team's values (no NaN among them).
+template <int L>
+__device__ __forceinline__ float team_max(float x) {
+  if constexpr (L == 32) {
+    float r;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(x));
+    return r;
+  } else {
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    for (int o = L / 2; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+    return x;
+  }
+}
+template <int L, typename R>
+__device__ __forceinline__ R team_sum(R x) {
+#pragma unroll
+  for (int o = L / 2; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
   return x;
+}
+// The lanes of the team on which p holds, and whether it holds on some.
+template <int L>
+__device__ __forceinline__ uint32_t team_ballot(bool p, int lane) {
+  const uint32_t b = __ballot_sync(0xffffffffu, p);
+  return L == 32 ? b : b >> (lane & ~(L - 1)) & ((1u << (L & 31)) - 1u);
+}
+template <int L>
+__device__ __forceinline__ bool team_any(bool p, int lane) {
+  return team_ballot<L>(p, lane) != 0;
+}
+
+// The k-th largest of the team's values.  Of a whole warp, equal values count
+// once (which gives a smaller one, or -inf).
+template <int L>
+__device__ __forceinline__ float team_kth(float x, int k, int lane) {
+  if constexpr (L == 32) {
+    float kth = -INFINITY;
+    for (int j = 0; j < k; ++j) {
+      kth = team_max<L>(x);
+      x = x == kth ? -INFINITY : x;
+    }
+    return kth;
+  } else {
+    // a bitonic sorting network, descending
+#pragma unroll
+    for (int size = 2; size <= L; size <<= 1)
+#pragma unroll
+      for (int o = size / 2; o >= 1; o >>= 1) {
+        const float y = __shfl_xor_sync(0xffffffffu, x, o);
+        const bool upper = (lane & o) != 0, up = size < L && (lane & size) != 0;
+        x = upper == up ? fmaxf(x, y) : fminf(x, y);
+      }
+    return __shfl_sync(0xffffffffu, x, k - 1, L);
+  }
 }
 
 // max(a, |b|), a NaN's place taken by NaN.
@@ -193,8 +239,8 @@ __device__ __forceinline__ float max_abs_nan(float a, float b) {
   return r;
 }
 
-// 2^x and 1/x by the approximate instructions, each within one unit in the
-// last place of 2^-22 or better, subnormals taken as zero.
+// 2^x (within 2^-22 relative) and 1/x (within 2^-23) by the approximate
+// instructions; subnormals are taken as zero.
 __device__ __forceinline__ float fast_exp2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -223,115 +269,38 @@ __device__ __forceinline__ R group_score(R a1, R a2, int group_top) {
   return group_top == 1 || a2 == -INFINITY ? a1 : a1 + a2;
 }
 
-// Scores of all groups for any group size: lane g gets group g's (-inf behind
-// the last).  v: the lane's V values, -inf where an expert cannot be chosen.
-template <typename R, int V>
-__device__ __forceinline__ R group_scores_any(const R (&v)[V], int lane, int n_group, int gsize, int group_top) {
+// Scores of all groups for any group size: lane g of the team gets group g's
+// (-inf behind the last).  v: the lane's V values, -inf where an expert cannot
+// be chosen.
+template <typename R, int L, int V>
+__device__ __forceinline__ R group_scores_any(const R (&v)[V], int tl, int n_group, int gsize, int group_top) {
   R mine = -INFINITY;
   for (int g = 0; g < n_group; ++g) {
     R a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int rel = lane * V + i - g * gsize;
+      const int rel = tl * V + i - g * gsize;
       if (rel >= 0 && rel < gsize) merge_top2(a1, a2, v[i], static_cast<R>(-INFINITY));
     }
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
+    for (int o = L / 2; o >= 1; o >>= 1) {
       const R b1 = __shfl_xor_sync(0xffffffffu, a1, o), b2 = __shfl_xor_sync(0xffffffffu, a2, o);
       merge_top2(a1, a2, b1, b2);
     }
-    if (lane == g) mine = group_score(a1, a2, group_top);
+    if (tl == g) mine = group_score(a1, a2, group_top);
   }
   return mine;
 }
 
 // ---------------------------------------------------------------- the choice in 64 bits
 
-// Chooses the experts of one row in 64 bits; lane j returns the expert of slot
-// j, or -1.  Rows come here when 32 bits cannot tell two values apart, so it
-// is kept out of line and written for size, not speed.
-template <typename LT, int V>
-__device__ __noinline__ int gate_choose64(const GateArgs& p, const LT* row, int lane) {
-  double c[V], k[V];
-  double top = -INFINITY;
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    c[i] = e < p.E ? static_cast<double>(gate_at(row, e)) : -INFINITY;
-    k[i] = c[i];
-    top = c[i] > top ? c[i] : top;
-  }
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    const double b = __shfl_xor_sync(0xffffffffu, top, o);
-    top = b > top ? b : top;
-  }
-  double total = 0.0;
-  if (!p.sigmoid) {
-#pragma unroll
-    for (int i = 0; i < V; ++i) total += exp(c[i] - top);
-    total = warp_sum(total);
-  }
-#pragma unroll
-  for (int i = 0; i < V; ++i) {
-    const int e = lane * V + i;
-    const bool dead = c[i] == -INFINITY || (p.bias && __ldg(p.bias + e) == -INFINITY);
-    const double s = p.sigmoid ? 1.0 / (1.0 + exp(-c[i])) : exp(c[i] - top) / total;
-    c[i] = dead ? -INFINITY : (p.bias ? s + static_cast<double>(__ldg(p.bias + e)) : s);
-    k[i] = p.bias || dead ? c[i] : k[i];  // without a bias the experts go by their logits
-  }
-  if (p.n_group > 1) {
-    const int gsize = p.gsize;
-    const double mine = group_scores_any<double, V>(c, lane, p.n_group, gsize, p.group_top);
-    int rank = 0;
-    for (int j = 0; j < p.n_group; ++j) {
-      const double o = __shfl_sync(0xffffffffu, mine, j);
-      rank += o > mine || (o == mine && j < lane);
-    }
-    const uint32_t kept = __ballot_sync(0xffffffffu, lane < p.n_group && rank < p.topk_group);
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (!((kept >> min(31, (lane * V + i) / gsize)) & 1)) k[i] = -INFINITY;
-  }
-  int mine_id = -1;
-  for (int j = 0; j < p.topk; ++j) {
-    double best = -INFINITY;
-    int at = 0x7FFFFFFF;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (k[i] > best) {
-        best = k[i];
-        at = lane * V + i;
-      }
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) {
-      const double b = __shfl_xor_sync(0xffffffffu, best, o);
-      const int a = __shfl_xor_sync(0xffffffffu, at, o);
-      if (b > best || (b == best && a < at)) {
-        best = b;
-        at = a;
-      }
-    }
-    if (best == -INFINITY) break;
-    if (lane == j) mine_id = at;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (lane * V + i == at) k[i] = -INFINITY;
-  }
-  return mine_id;
-}
-
-// ---------------------------------------------------------------- forward
-
-// Sum of exp(l - top) over the row in 64 bits (every lane returns it).
-template <typename LT, int V>
-__device__ __noinline__ double gate_total64(const LT* row, int E, int lane, float top) {
+// Sum of exp(l - top) over the row in 64 bits (every lane of the team returns it).
+template <typename LT, int L>
+__device__ __noinline__ double gate_total64(const LT* row, int E, int tl, float top) {
   double sum = 0.0;
-  for (int i = 0; i < V; ++i) {
-    const int e = lane + 32 * i;
-    if (e < E) sum += exp(static_cast<double>(gate_at(row, e)) - static_cast<double>(top));
-  }
-  return warp_sum(sum);
+  for (int e = tl; e < (E + L - 1) / L * L; e += L)
+    sum += e < E ? exp(static_cast<double>(gate_at(row, e)) - static_cast<double>(top)) : 0.0;
+  return team_sum<L>(sum);
 }
 
 // c of expert e in 64 bits; total64 from gate_total64 (softmax only).
@@ -342,14 +311,69 @@ __device__ __noinline__ double gate_score64(const GateArgs& p, const LT* row, in
   return p.bias ? s + static_cast<double>(__ldg(p.bias + e)) : s;
 }
 
-// One warp a token.
-//
-// Error of a 32-bit score (u = 2^-24).  ex2.approx and rcp.approx are within
-// 2^-22 = 4u relative; the argument x log2(e) of ex2 is off by 2u |x| log2(e)
-// (the constant's rounding and the product's), which is 2u |x| relative in the
-// exponential.
-//   sigmoid  s(1-s)(4 + 2|l|) u <= (1 + 0.45) u, the sum u, the quotient 4u:
-//            below 7u.
+// Chooses the experts of a row in 64 bits; lane j of the team returns the
+// expert of slot j, or -1.  Rows come here when 32 bits cannot tell values
+// apart and more than the listed candidates are in question, so it is kept out
+// of line and written for size, not speed.
+template <typename LT, int L, int V>
+__device__ __noinline__ int gate_choose64(const GateArgs& p, const LT* row, int tl, float top) {
+  double c[V], k[V];
+  const double total = p.sigmoid ? 1.0 : gate_total64<LT, L>(row, p.E, tl, top);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int e = tl * V + i;
+    const double x = e < p.E ? static_cast<double>(gate_at(row, e)) : -INFINITY;
+    const bool dead = x == -INFINITY || (p.bias && __ldg(p.bias + e) == -INFINITY);
+    c[i] = dead ? -INFINITY : gate_score64(p, row, e, top, total);
+    k[i] = p.bias || dead ? c[i] : x;  // without a bias the experts go by their logits
+  }
+  if (p.n_group > 1) {
+    const double mine = group_scores_any<double, L, V>(c, tl, p.n_group, p.gsize, p.group_top);
+    int rank = 0;
+    for (int j = 0; j < p.n_group; ++j) {
+      const double o = __shfl_sync(0xffffffffu, mine, j, L);
+      rank += o > mine || (o == mine && j < tl);
+    }
+    const bool kept = tl < p.n_group && rank < p.topk_group;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (!__shfl_sync(0xffffffffu, kept, min(L - 1, (tl * V + i) / p.gsize), L)) k[i] = -INFINITY;
+  }
+  int mine_id = -1;
+  for (int j = 0; j < p.topk; ++j) {
+    double best = -INFINITY;
+    int at = 0x7FFFFFFF;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (k[i] > best) {
+        best = k[i];
+        at = tl * V + i;
+      }
+#pragma unroll
+    for (int o = L / 2; o >= 1; o >>= 1) {
+      const double b = __shfl_xor_sync(0xffffffffu, best, o);
+      const int a = __shfl_xor_sync(0xffffffffu, at, o);
+      if (b > best || (b == best && a < at)) {
+        best = b;
+        at = a;
+      }
+    }
+    if (tl == j && best > -INFINITY) mine_id = at;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (tl * V + i == at) k[i] = -INFINITY;
+  }
+  return mine_id;
+}
+
+// ---------------------------------------------------------------- forward
+
+// Error of a 32-bit score (u = 2^-24).  ex2.approx is within 2^-22 = 4u
+// relative, rcp.approx within 2^-23 = 2u; the argument x log2(e) of ex2 is off
+// by 2u |x| log2(e) (the constant's rounding and the product's), which is 2u |x|
+// relative in the exponential.
+//   sigmoid  s(1-s)(4 + 2|l|) u <= (1 + 0.45) u, the sum u, the quotient 2u:
+//            below 5u.
 //   softmax  p |x| 2u <= 0.74u and 4u p from the exponential; from the sum (at
 //            most 1024 terms, in 64 bits (2 + 2 * 6.94) u of their own and 37 u
 //            of additions) and the quotient 60u p: <= p 2^-17 + u.
@@ -359,30 +383,36 @@ __device__ __noinline__ double gate_score64(const GateArgs& p, const LT* row, in
 //
 // The choice.  The topk-th largest of the lanes' best values is a lower bound
 // of the topk-th best value of the row, since so many values reach it, and few
-// values do (for 256 experts, topk 8: about ten).  Those (and the ones closer
-// below it than `near`) are put together in shared memory, one a lane, and each
+// values do (for 256 experts, topk 8: about eleven).  Those (and the ones
+// closer below it than `near`) are put together in shared memory, and each
 // lane counts the ones before its own.  That takes the place of topk rounds of
 // finding and removing the best (which serve the rows with more than 32).
-template <typename LT, int V, bool SIGMOID, bool BIAS>
+template <typename LT, int L, int V, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_constant__ GateArgs p) {
-  __shared__ float2 cand[kGateWarps][32 * V];  // value, expert
-  __shared__ int count[kGateWarps];
+  constexpr int kTeams = 32 * kGateWarps / L;
+  constexpr int kOwn = kGateList / L;            // listed experts of a lane
+  __shared__ float2 lists[kTeams][L * V];        // value, expert
+  __shared__ int counts[kTeams];
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31;
-  const int warp = threadIdx.x >> 5;
-  float2* list = cand[warp];
-  const int t = blockIdx.x * kGateWarps + warp;
-  if (t >= p.T) return;
-  const LT* row = static_cast<const LT*>(p.logits) + static_cast<size_t>(t) * p.E;
+  const int tl = threadIdx.x & (L - 1);
+  const int team = threadIdx.x / L;
+  float2* list = lists[team];
+  int* count = counts + team;
+  const int t0 = blockIdx.x * kTeams + (threadIdx.x >> 5) * (32 / L);  // the warp's first token
+  if (t0 >= p.T) return;
+  const int t = t0 + (L == 32 ? 0 : lane / L);
+  const bool mine_is = t < p.T;  // (a last odd token leaves a team without one)
+  const LT* row = static_cast<const LT*>(p.logits) + static_cast<size_t>(mine_is ? t : t0) * p.E;
 
   const bool sums = p.n_group > 1 && p.group_top > 1;
   const bool scored = BIAS || sums;
-  const bool full = p.E == 32 * V;  // every lane holds V experts
-  const int live = full ? V : min(V, max(0, p.E - lane * V));
+  const bool full = p.E == L * V;  // every lane holds V experts
+  const int live = full ? V : min(V, max(0, p.E - tl * V));
   float l[V], c[V];
-  gate_load_row<V>(row, p.E, lane, -FLT_MAX, l);
-  if (BIAS) gate_load_row<V>(p.bias, p.E, lane, 0.0f, c);
+  gate_load_row<V>(row, p.E, tl, -FLT_MAX, l);
+  if (BIAS) gate_load_row<V>(p.bias, p.E, tl, 0.0f, c);
   float big = 0.0f, largest = 0.0f;  // the largest |logit| and |bias|: below infinity when nothing is masked or bad
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -394,12 +424,12 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
     float m = l[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
-    top = warp_max(m);
+    top = team_max<L>(m);
     if (top == -INFINITY) top = 0.0f;
     float sum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) sum += i < live ? expf(l[i] - top) : 0.0f;
-    total = warp_sum(sum);
+    total = team_sum<L>(sum);
   }
   float near = 0.0f;
   if (scored) {
@@ -409,7 +439,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       const float s = SIGMOID ? fast_rcp(1.0f + fast_exp2(-kLog2e * l[i])) : fast_exp2(kLog2e * (l[i] - top)) * inv;
       c[i] = BIAS ? s + c[i] : s;
     }
-    near = 0x1p-20f + (SIGMOID ? 0.0f : 0x1p-16f * inv);
+    near = 0x1.4p-21f + (SIGMOID ? 0.0f : 0x1p-16f * inv);  // 10u
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) c[i] = l[i];
@@ -422,24 +452,22 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       bad |= i < live && !(l[i] < INFINITY);
       if (l[i] == -INFINITY) c[i] = -INFINITY;
       if (BIAS) {
-        const float b = i < live ? __ldg(p.bias + lane * V + i) : 0.0f;
+        const float b = i < live ? __ldg(p.bias + tl * V + i) : 0.0f;
         bad |= !(b < INFINITY);
         if (b == -INFINITY) c[i] = -INFINITY;
         largest = fmaxf(i == 0 ? 0.0f : largest, b > -INFINITY ? fabsf(b) : 0.0f);
       }
     }
-    if (__any_sync(0xffffffffu, bad)) {
-      // NaN or +inf among the logits or the bias: the token is not routed
-      if (lane == 0) atomicOr(&g_dg_error, 0x20);
-      if (lane < p.topk) {
-        p.ids[static_cast<size_t>(t) * p.topk + lane] = -1;
-        p.weights[static_cast<size_t>(t) * p.topk + lane] = 0.0f;
-      }
-      return;
+    if (team_any<L>(bad, lane)) {
+      // NaN or +inf among the logits or the bias: no expert can be chosen
+      if (tl == 0) atomicOr(&g_dg_error, 0x20);
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = -INFINITY;
+      largest = 0.0f;
     }
   }
   if (BIAS) {
-    largest = warp_max(largest);
+    largest = team_max<L>(largest);
     near += 0x1p-23f * (1.0f + largest);
   }
   if (!full) {
@@ -448,10 +476,11 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       if (i >= live) c[i] = -INFINITY;
   }
 
-  bool unsure = false;  // the row needs the choice in 64 bits (all lanes agree)
+  bool unsure = false;  // the token needs the choice in 64 bits (the team agrees)
   if (p.n_group > 1) {
     const bool whole = p.span_log2 >= 0;
     const int span = whole ? 1 << p.span_log2 : 1;  // lanes that hold the same group
+    const int at = whole ? tl >> p.span_log2 : tl;  // the group whose score this lane holds
     float mine;
     float a1 = c[0], a2 = -INFINITY;
     if (whole) {
@@ -467,32 +496,32 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       }
       mine = group_score(a1, a2, p.group_top);
     } else {
-      mine = group_scores_any<float, V>(c, lane, p.n_group, p.gsize, p.group_top);
+      mine = group_scores_any<float, L, V>(c, tl, p.n_group, p.gsize, p.group_top);
     }
     // lanes behind the last group have -inf, as groups without an expert to choose
+    const bool some = mine > -INFINITY;
     const float gnear = scored ? 2.0f * near + 0x1p-21f * (1.0f + largest) : 0.0f;
-    // the topk_group-th best score (equal ones once), and the best below it
-    float rest = mine, kth = -INFINITY;
-    for (int j = 0; j < p.topk_group; ++j) {
-      kth = warp_max(rest);
-      rest = rest == kth ? -INFINITY : rest;
-    }
-    bool kept = mine >= kth && mine > -INFINITY;
-    const bool close = scored && kth - warp_max(rest) <= gnear;  // (-inf - -inf is NaN: not close)
-    if (close || __popc(__ballot_sync(0xffffffffu, kept)) > p.topk_group * span) {
-      // a close call or equal scores: rank the groups one by one
-      const int at = whole ? lane >> p.span_log2 : lane;
-      const bool some = mine > -INFINITY;
+    // the topk_group-th best score, and the best below it
+    const float kth = team_kth<L>(mine, L == 32 ? p.topk_group : p.topk_group * span, lane);
+    bool kept = some && mine >= kth;
+    const float below = team_max<L>(mine < kth ? mine : -INFINITY);
+    // (every lane votes, whatever its team found: no vote behind a condition that teams may differ in)
+    const int lanes_kept = __popc(team_ballot<L>(kept, lane));
+    const bool slow = (scored && kth - below <= gnear) ||  // (-inf - -inf is NaN: not close)
+                      lanes_kept > p.topk_group * span;
+    if (__any_sync(0xffffffffu, slow)) {
+      // a close call, or equal scores: rank the groups one by one
       int above = 0, sure_above = 0, maybe_above = 0;
       for (int j = 0; j < p.n_group; ++j) {
-        const float o = __shfl_sync(0xffffffffu, mine, j * span);
+        const float o = __shfl_sync(0xffffffffu, mine, j * span, L);
         above += o > mine || (o == mine && j < at);
         sure_above += o > mine + gnear;
         maybe_above += j != at && o >= mine - gnear;
       }
-      kept = some && above < p.topk_group;
-      unsure = scored && __any_sync(0xffffffffu, some && maybe_above >= p.topk_group && sure_above < p.topk_group);
-      if (unsure && whole) {
+      if (slow) kept = some && above < p.topk_group;
+      // is a kept group too close to one that is not?
+      unsure = team_any<L>(scored && some && maybe_above >= p.topk_group && sure_above < p.topk_group, lane);
+      if (__any_sync(0xffffffffu, unsure) && whole) {
         // The groups' scores in 64 bits, from the one or two experts that each
         // is made of, if 32 bits tell those from the group's others.
         const float lowest = (p.group_top == 1 || a2 == -INFINITY ? a1 : a2) - near;
@@ -501,7 +530,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
         for (int i = 0; i < V; ++i)
           if (c[i] >= lowest && c[i] > -INFINITY) {
             e2 = e1;
-            e1 = lane * V + i;
+            e1 = tl * V + i;
             ++n;
           }
         for (int o = 1; o < span; o <<= 1) {
@@ -513,19 +542,23 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
           e2 = x2;
         }
         const int want = p.group_top == 1 || a2 == -INFINITY ? 1 : 2;
-        if (__all_sync(0xffffffffu, !some || n == want)) {
-          const double total64 = SIGMOID ? 1.0 : gate_total64<LT, V>(row, p.E, lane, top);
-          double exact = -INFINITY;
-          if (some) {
-            exact = gate_score64(p, row, e1, top, total64);
-            if (want == 2) exact += gate_score64(p, row, e2, top, total64);
-          }
-          __syncwarp();
-          above = 0;
-          for (int j = 0; j < p.n_group; ++j) {
-            const double o = __shfl_sync(0xffffffffu, exact, j * span);
-            above += o > exact || (o == exact && j < at);
-          }
+        const bool told = !team_any<L>(some && n != want, lane);
+        const double total64 = SIGMOID ? 1.0 : gate_total64<LT, L>(row, p.E, tl, top);
+        // of two experts, one by the odd lanes and one by the even ones
+        const bool use = some && unsure && told;
+        const bool second = want == 2 && span > 1 && (tl & 1);
+        double exact = use ? gate_score64(p, row, second ? max(e1, e2) : want == 2 ? min(e1, e2) : e1, top, total64)
+                           : -INFINITY;
+        __syncwarp();
+        const double other = __shfl_xor_sync(0xffffffffu, exact, 1);
+        if (use && want == 2) exact += span > 1 ? other : gate_score64(p, row, max(e1, e2), top, total64);
+        __syncwarp();
+        above = 0;
+        for (int j = 0; j < p.n_group; ++j) {
+          const double o = __shfl_sync(0xffffffffu, exact, j * span, L);
+          above += o > exact || (o == exact && j < at);
+        }
+        if (unsure && told) {
           kept = some && above < p.topk_group;
           unsure = false;
         }
@@ -535,10 +568,9 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
 #pragma unroll
       for (int i = 0; i < V; ++i) c[i] = kept ? c[i] : -INFINITY;
     } else {
-      const uint32_t all_kept = __ballot_sync(0xffffffffu, kept);
 #pragma unroll
       for (int i = 0; i < V; ++i)
-        if (!((all_kept >> min(31, (lane * V + i) / p.gsize)) & 1)) c[i] = -INFINITY;
+        if (!__shfl_sync(0xffffffffu, kept, min(L - 1, (tl * V + i) / p.gsize), L)) c[i] = -INFINITY;
     }
     if (!BIAS && sums) {  // the groups went by scores, their experts go by the logits
 #pragma unroll
@@ -547,118 +579,154 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
   }
 
   int mine_id = -1;
-  if (!unsure) {
-    float best = c[0];
+  float best = c[0];
 #pragma unroll
-    for (int i = 1; i < V; ++i) best = fmaxf(best, c[i]);
-    if (lane == 0) count[warp] = 0;
-    float kth = -INFINITY;
-    for (int j = 0; j < p.topk; ++j) {
-      kth = warp_max(best);
-      best = best == kth ? -INFINITY : best;
+  for (int i = 1; i < V; ++i) best = fmaxf(best, c[i]);
+  if (tl == 0) *count = 0;
+  const float kth = team_kth<L>(best, p.topk, lane);
+  // (-FLT_MAX where fewer lanes than topk have an expert: every one is in question)
+  const float bound = kth == -INFINITY ? -FLT_MAX : BIAS ? kth - near : kth;
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i) n += c[i] >= bound;
+  __syncwarp();
+  int pos = n > 0 ? atomicAdd(count, n) : 0;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+    if (c[i] >= bound) list[pos++] = make_float2(c[i], __int_as_float(tl * V + i));
+  __syncwarp();
+  const int all = *count;
+  const int m = min(all, kGateList);
+  const float2 none = make_float2(-INFINITY, __int_as_float(-1));
+  float2 x[kOwn];
+  int rank[kOwn];
+  if constexpr (L == 32) {
+    // the place of candidate `lane`, or of lane % 16 from half of the others where no more than 16 are
+    const bool two = m <= 16;
+    const int own = two ? tl & 15 : tl;
+    x[0] = own < m ? list[own] : none;
+    rank[0] = 0;
+    for (int j = two ? tl >> 4 : 0; j < m; j += two ? 2 : 1) {
+      const float2 o = list[j];
+      rank[0] += o.x > x[0].x || (o.x == x[0].x && __float_as_int(o.y) < __float_as_int(x[0].y));
     }
-    // (-FLT_MAX where fewer lanes than topk have an expert: every one is in question)
-    const float bound = kth == -INFINITY ? -FLT_MAX : BIAS ? kth - near : kth;
-    int n = 0;
+    if (two) rank[0] += __shfl_xor_sync(0xffffffffu, rank[0], 16);
+  } else {
+    // both teams count to the longer list, the shorter one filled up
+    const int longest = __reduce_max_sync(0xffffffffu, m);
 #pragma unroll
-    for (int i = 0; i < V; ++i) n += c[i] >= bound;
+    for (int r = 0; r < kOwn; ++r) {
+      const int own = tl + L * r;
+      x[r] = own < m ? list[own] : none;
+      if (own >= m && own < longest) list[own] = none;
+      rank[r] = 0;
+    }
     __syncwarp();
-    int pos = n > 0 ? atomicAdd(&count[warp], n) : 0;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
-      if (c[i] >= bound) list[pos++] = make_float2(c[i], __int_as_float(lane * V + i));
-    __syncwarp();
-    const int m = count[warp];
-    if (m <= 32) {
-      // the place of candidate `lane` (of lane % 16, from half of the others, where no more than 16 are)
-      const bool two = m <= 16;
-      const int own = two ? lane & 15 : lane;
-      const float2 x = own < m ? list[own] : make_float2(-INFINITY, 0.0f);
-      int rank = 0;
-      for (int j = two ? lane >> 4 : 0; j < m; j += two ? 2 : 1) {
-        const float2 o = list[j];
-        rank += o.x > x.x || (o.x == x.x && __float_as_int(o.y) < __float_as_int(x.y));
+    for (int r = 0; r < kOwn; ++r)
+      if (r == 0 || longest > L * r)
+        for (int j = 0; j < longest; ++j) {
+          const float2 o = list[j];
+          rank[r] += o.x > x[r].x || (o.x == x[r].x && __float_as_int(o.y) < __float_as_int(x[r].y));
+        }
+  }
+  __syncwarp();
+#pragma unroll
+  for (int r = 0; r < kOwn; ++r)
+    if (tl + L * r < m) list[rank[r]] = x[r];
+  __syncwarp();
+  const float2 y = tl < m ? list[tl] : none;
+  mine_id = tl < p.topk ? __float_as_int(y.y) : -1;
+  if (BIAS) {
+    // neighbours in the order, down to the first behind the chosen ones
+    const bool near_one = tl < p.topk && tl + 1 < m && y.x - list[tl + 1].x <= near;
+    if (__any_sync(0xffffffffu, near_one)) {
+      const bool found_near = team_any<L>(near_one, lane);
+      const bool redo = found_near && all <= kGateList;
+      const double total64 = SIGMOID ? 1.0 : gate_total64<LT, L>(row, p.E, tl, top);
+      double z[kOwn];
+#pragma unroll
+      for (int r = 0; r < kOwn; ++r) {
+        z[r] = redo && tl + L * r < m ? gate_score64(p, row, __float_as_int(x[r].y), top, total64) : -INFINITY;
+        rank[r] = 0;
       }
       __syncwarp();
-      if (two) rank += __shfl_xor_sync(0xffffffffu, rank, 16);
-      if (lane < m) list[rank] = x;
+      const int longest = __reduce_max_sync(0xffffffffu, m);
+#pragma unroll
+      for (int q = 0; q < kOwn; ++q)
+        for (int j = 0; j < min(L, longest - L * q); ++j) {
+          const double o = __shfl_sync(0xffffffffu, z[q], j, L);
+          const int oe = __shfl_sync(0xffffffffu, __float_as_int(x[q].y), j, L);
+#pragma unroll
+          for (int r = 0; r < kOwn; ++r) rank[r] += o > z[r] || (o == z[r] && oe < __float_as_int(x[r].y));
+        }
+#pragma unroll
+      for (int r = 0; r < kOwn; ++r)
+        if (redo && tl + L * r < m) list[rank[r]] = x[r];
       __syncwarp();
-      float2 y = lane < m ? list[lane] : make_float2(-INFINITY, __int_as_float(-1));
-      if (BIAS) {
-        // neighbours in the order, down to the first behind the chosen ones
-        const float next = __shfl_down_sync(0xffffffffu, y.x, 1);
-        if (__any_sync(0xffffffffu, lane < p.topk && lane + 1 < m && y.x - next <= near)) {
-          const int e = __float_as_int(y.y);
-          const double total64 = SIGMOID ? 1.0 : gate_total64<LT, V>(row, p.E, lane, top);
-          const double z = lane < m ? gate_score64(p, row, e, top, total64) : -INFINITY;
-          __syncwarp();
-          rank = 0;
-          for (int j = 0; j < m; ++j) {
-            const double o = __shfl_sync(0xffffffffu, z, j);
-            const int oe = __shfl_sync(0xffffffffu, e, j);
-            rank += o > z || (o == z && oe < e);
-          }
-          if (lane < m) list[rank] = y;
-          __syncwarp();
-          if (lane < m) y = list[lane];
-        }
-      }
-      mine_id = lane < p.topk ? __float_as_int(y.y) : -1;
-    } else {
-      // more than 32 in question: the best of the warp, topk times; one more
-      // shows whether the last place was a close one
-      const int rounds = BIAS ? p.topk + 1 : p.topk;
-      float before = INFINITY;
-      for (int j = 0; j < rounds; ++j) {
-        float lead = c[0];
-#pragma unroll
-        for (int i = 1; i < V; ++i) lead = fmaxf(lead, c[i]);
-        const float all = warp_max(lead);
-        if (all == -INFINITY) break;
-        if (BIAS && before - all <= near) {
-          unsure = true;
-          break;
-        }
-        before = all;
-        const int src = __ffs(__ballot_sync(0xffffffffu, lead == all)) - 1;
-        int at = 0;
-        if (lane == src) {
-          bool found = false;
-#pragma unroll
-          for (int i = 0; i < V; ++i)
-            if (!found && c[i] == all) {
-              found = true;
-              c[i] = -INFINITY;
-              at = lane * V + i;
-            }
-        }
-        at = __shfl_sync(0xffffffffu, at, src);
-        if (lane == j && j < p.topk) mine_id = at;
-      }
+      if (redo && tl < min(m, p.topk)) mine_id = __float_as_int(list[tl].y);
     }
   }
-  if (unsure) mine_id = gate_choose64<LT, V>(p, row, lane);
+  if (__any_sync(0xffffffffu, all > kGateList)) {
+    // more than 32 in question: the best of the team, topk times; one more
+    // shows whether the last place was a close one
+    const int rounds = BIAS ? p.topk + 1 : p.topk;
+    float before = INFINITY;
+    bool close = false;
+    int found_id = -1;
+    for (int j = 0; j < rounds; ++j) {
+      float lead = c[0];
+#pragma unroll
+      for (int i = 1; i < V; ++i) lead = fmaxf(lead, c[i]);
+      const float next = team_max<L>(lead);
+      close |= BIAS && next > -INFINITY && before - next <= near;
+      before = next;
+      const uint32_t who = __ballot_sync(0xffffffffu, lead == next && next > -INFINITY) >> (lane & ~(L - 1));
+      const int src = __ffs(L == 32 ? who : who & ((1u << (L & 31)) - 1u)) - 1;  // -1: none is left
+      int e = -1;
+      if (tl == src) {
+        bool found = false;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (!found && c[i] == next) {
+            found = true;
+            c[i] = -INFINITY;
+            e = tl * V + i;
+          }
+      }
+      e = __shfl_sync(0xffffffffu, e, src < 0 ? 0 : src, L);
+      if (tl == j && j < p.topk && src >= 0) found_id = e;
+    }
+    if (all > kGateList) {
+      mine_id = found_id;
+      unsure |= close;
+    }
+  }
+  if (__any_sync(0xffffffffu, unsure)) {
+    const int id = gate_choose64<LT, L, V>(p, row, tl, top);
+    if (unsure) mine_id = id;
+  }
 
   const bool has = mine_id >= 0;
-  const float x = has ? gate_at(row, mine_id) : -INFINITY;
+  const float s = has ? gate_at(row, mine_id) : -INFINITY;  // the chosen expert's logit
   float w;
   if (p.renorm) {
     // s_j / sum s; from the ratios to the largest, where the scores might underflow
-    const float m = warp_max(x);
+    const float hi = team_max<L>(s);
     float v;
-    if (!SIGMOID) v = expf(x - m);
-    else if (m > -60.0f) v = __fdiv_rn(1.0f, 1.0f + expf(-x));
-    else v = __fdiv_rn(expf(x - m), 1.0f + expf(x));
+    if (!SIGMOID) v = expf(s - hi);
+    else if (hi > -60.0f) v = __fdiv_rn(1.0f, 1.0f + expf(-s));
+    else v = __fdiv_rn(expf(s - hi), 1.0f + expf(s));
     v = has ? v : 0.0f;
-    w = __fdiv_rn(v, warp_sum(v));
+    w = __fdiv_rn(v, team_sum<L>(v));
   } else if (SIGMOID) {
-    w = __fdiv_rn(expf(fminf(x, 0.0f)), 1.0f + expf(-fabsf(x)));
+    w = __fdiv_rn(expf(fminf(s, 0.0f)), 1.0f + expf(-fabsf(s)));
   } else {
-    w = __fdiv_rn(expf(x - top), total);
+    w = __fdiv_rn(expf(s - top), total);
   }
-  if (lane < p.topk) {
-    p.ids[static_cast<size_t>(t) * p.topk + lane] = mine_id;
-    p.weights[static_cast<size_t>(t) * p.topk + lane] = has ? p.scale * w : 0.0f;
+  if (mine_is && tl < p.topk) {
+    p.ids[static_cast<size_t>(t) * p.topk + tl] = mine_id;
+    p.weights[static_cast<size_t>(t) * p.topk + tl] = has ? p.scale * w : 0.0f;
   }
 }
 
@@ -696,14 +764,14 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(cons
     const float inv = __fdiv_rn(1.0f, 1.0f + tail);
     const float rest = (x < 0.0f ? 1.0f : tail) * inv;
     if (p.renorm) {
-      float m = warp_max(x);
+      float m = team_max<32>(x);
       if (m == -INFINITY) m = 0.0f;
       // s / sum s as in the forward pass
       float r = p.sigmoid ? expf(fminf(x, 0.0f) - fminf(m, 0.0f)) * inv : expf(x - m);
       r = has ? r : 0.0f;
-      const float sum = warp_sum(r);
+      const float sum = team_sum<32>(r);
       r = sum > 0.0f ? __fdiv_rn(r, sum) : 0.0f;
-      const float mean = warp_sum(r * g);
+      const float mean = team_sum<32>(r * g);
       v = p.scale * r * (p.sigmoid ? rest : 1.0f) * (g - mean);
     } else {
       v = p.scale * ((x < 0.0f ? tail : 1.0f) * inv) * rest * g;
@@ -744,7 +812,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(cons
     float m = l[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
-    m = warp_max(m);
+    m = team_max<32>(m);
     if (m == -INFINITY) m = 0.0f;
     float sum = 0.0f;
 #pragma unroll
@@ -752,7 +820,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(cons
       l[i] = expf(l[i] - m);
       sum += l[i];
     }
-    sum = warp_sum(sum);
+    sum = team_sum<32>(sum);
     const float inv = sum > 0.0f ? 1.0f / sum : 0.0f;
     float mean = 0.0f;
 #pragma unroll
@@ -760,7 +828,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(cons
       l[i] *= inv;
       mean += l[i] * o[i];
     }
-    mean = warp_sum(mean);
+    mean = team_sum<32>(mean);
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = p.scale * l[i] * (o[i] - mean);
   }

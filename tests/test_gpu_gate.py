@@ -123,6 +123,30 @@ def test_scores_that_32_bits_cannot_tell_apart():
     check_gate(l, 8, torch.zeros(96), score="sigmoid")
 
 
+@pytest.mark.parametrize("E,n_group,topk_group,topk", [(64, 4, 2, 4), (64, 1, 1, 6), (32, 4, 2, 8), (128, 1, 1, 8),
+                                                       (128, 8, 4, 4), (60, 6, 2, 3), (100, 5, 2, 8), (256, 8, 4, 8)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_neighbouring_tokens_that_take_different_ways(E, n_group, topk_group, topk, score):
+    """Tokens that need 64 bits, tokens that do not, equal logits, padding and
+    rows that are not numbers side by side: two tokens may share a warp."""
+    T = 301
+    l = _rand(1, E, 23).repeat(T, 1)
+    s = routing.scores(_f64(l[:1]), score)[0]
+    b = torch.from_numpy((1.0 - s).astype(np.float32))
+    rng = np.random.default_rng(E)
+    kind = torch.from_numpy(rng.integers(0, 6, T))
+    other = _rand(T, E, 24)
+    l[kind == 1] = other[kind == 1]
+    l[kind == 2] = -INF
+    l[kind == 3] = 0.25
+    l[kind == 4, ::2] = -INF
+    l[(kind == 5).nonzero()[:3, 0], E - 1] = float("nan")
+    for group_top in (1, 2):
+        for bias in (b, None, torch.zeros(E)):
+            check_gate(l, topk, bias, score=score, renormalize=True, n_group=n_group, topk_group=topk_group,
+                       group_top=group_top)
+
+
 def test_masks_and_padding():
     T, E, topk = 40, 64, 6
     l = _rand(T, E, 31)
