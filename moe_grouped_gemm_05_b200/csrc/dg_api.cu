@@ -652,7 +652,7 @@ static const Config* int8_config_table(int* count) {
   static const Config table[] = {
       make_int8_config<64, 8, mode, 1, f32>(), make_int8_config<128, 6, mode, 1, f32>(),
       make_int8_config<256, 4, mode, 1, f32>(), make_int8_config<128, 8, mode, 2, f32>(),
-      make_int8_config<256, 6, mode, 2, f32>(),
+      make_int8_config<256, 6, mode, 2, f32>(), make_int8_config<224, 6, mode, 2, f32>(),
   };
   *count = static_cast<int>(sizeof(table) / sizeof(table[0]));
   return table;
@@ -662,7 +662,7 @@ static const Config* int8_config_table(int* count) {
 // in the FP8 kernels' cost model.
 static const CostParams kCostInt8[] = {
     {64, 1, 1, false, 200, 600},  {128, 1, 1, false, 210, 750},   {256, 1, 1, false, 330, 1300},
-    {128, 2, 1, false, 220, 900}, {256, 2, 1, false, 310, 1500},
+    {128, 2, 1, false, 220, 900}, {256, 2, 1, false, 310, 1500}, {224, 2, 1, false, 271, 1400},
 };
 
 template <int MODE>

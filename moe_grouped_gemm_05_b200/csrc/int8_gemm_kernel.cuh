@@ -233,8 +233,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     uint8_t* buf = smem + L::kOffEpi + epi * L::kEpiBuf;
     const uint32_t empty0 = kPair ? mapa_shared(smem_u32(tmem_empty), 0) : smem_u32(tmem_empty);
     constexpr int kChunks = BN / 32;
-    constexpr int kMine = kChunks / 2;
-    static_assert(kChunks % 2 == 0, "both warps of a quarter take the same number of chunks");
+    constexpr int kMine = (kChunks + 1) / 2;  // of the first warp; an odd last chunk is its own
     uint32_t own = 0;
     for (int t = unit0; t < ntiles; t += units) {
       const Tile tl = tile_of<MODE, L::kTileM>(t, p, prefix, counts);
@@ -342,8 +341,8 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         for (int i = 0; i < kMine; ++i) {
           const int c = half + 2 * i;
           const int col0 = n0 + 32 * c;
-          if (col0 >= p.N) break;
-          if (i + 1 < kMine && col0 + 64 < p.N) tmem_ld_32x32b_x32(t_row + 32 * (c + 2), r[(i + 1) & 1]);
+          if (c >= kChunks || col0 >= p.N) break;
+          if (c + 2 < kChunks && col0 + 64 < p.N) tmem_ld_32x32b_x32(t_row + 32 * (c + 2), r[(i + 1) & 1]);
           finish(r[i & 1], col0);
           tmem_wait_ld();
         }
