@@ -785,18 +785,24 @@ static int check_int8(const void* a, const float* sa, const void* b, const float
 
 // ------------------------------------------------------------------ launches of the row kernels
 
-// quantize_int8_kernel over rows of K elements.  Units of 16 elements: one a
-// thread up to 512 threads, then two (and four in BF16, 32 registers) a thread
-// of up to 1024; a longer row is read twice.  Rows of one warp share a block of four.
+// quantize_int8_kernel over rows of K elements, in units of 16.  Four units a
+// thread keep 128 bytes of BF16 in flight for each (32768x7168: 101 us, one unit
+// a thread 118, two 105, eight 101; permuted 16384x7168 top-2: 77 us against 91,
+// 95 and 107); longer rows than 1024 threads hold are read twice.  Few rows are
+// spread over more threads instead, one unit each (64x7168: 1.6 us against 2.0;
+// 592 rows 2.6 against 2.8, 1184 rows 4.4 against 4.2).
+constexpr int kFewRows = 592;
 template <typename T, bool PERM>
 static cudaError_t launch_quantize_int8(const QuantArgs& p, cudaStream_t st) {
   const int units = p.K / 16;
-  const int u = units <= 512 ? 1 : units <= 2048 ? 2 : (sizeof(T) == 2 && units <= 4096) ? 4 : 0;
+  constexpr bool half = sizeof(T) == 2;
+  const bool few = p.M <= kFewRows && units <= 512;
+  const int u = few || units <= 32 ? 1 : units <= 64 ? 2 : units <= (half ? 4096 : 2048) ? 4 : 0;
   const int warps = u == 0 ? 32 : (units + 32 * u - 1) / (32 * u);
   const int teams = warps == 1 ? 4 : 1;
   auto fn = u == 1   ? &quantize_int8_kernel<T, 1, PERM>
             : u == 2 ? &quantize_int8_kernel<T, 2, PERM>
-            : u == 4 ? &quantize_int8_kernel<T, sizeof(T) == 2 ? 4 : 0, PERM>
+            : u == 4 ? &quantize_int8_kernel<T, 4, PERM>
                      : &quantize_int8_kernel<T, 0, PERM>;
   LaunchAttrs la(1);
   cudaLaunchConfig_t lc = {};
@@ -806,6 +812,17 @@ static cudaError_t launch_quantize_int8(const QuantArgs& p, cudaStream_t st) {
   lc.attrs = la.attr;
   lc.numAttrs = la.n;
   return cudaLaunchKernelEx(&lc, fn, p);
+}
+
+// A block a token, and enough for the padding rows of many experts.
+template <typename T>
+static cudaError_t launch_quantize_permute_few(const QuantArgs& p, int sms, cudaStream_t st) {
+  const int units = p.K / 16;
+  const long long blocks = std::max<long long>(p.M, std::min<long long>(sms, (p.M_cap + kFewThreads - 1) / kFewThreads));
+  if (units <= kFewThreads) return launch_plain(quantize_permute_few_kernel<T, 1>, blocks, kFewThreads, st, p);
+  if (units <= 2 * kFewThreads) return launch_plain(quantize_permute_few_kernel<T, 2>, blocks, kFewThreads, st, p);
+  if (units <= 4 * kFewThreads) return launch_plain(quantize_permute_few_kernel<T, 4>, blocks, kFewThreads, st, p);
+  return launch_plain(quantize_permute_few_kernel<T, 0>, blocks, kFewThreads, st, p);
 }
 
 // The gate kernel for teams of L lanes with V experts each.
@@ -1388,11 +1405,6 @@ int dg_moe_quantize_permute_int8(const int32_t* topk_ids, int T, int topk, int n
   int r = device_info(&di);
   if (r) return r;
   auto st = static_cast<cudaStream_t>(stream);
-  // the scales are words of one K group: zero bits are the scale 0 of padding rows
-  if ((r = launch_route(topk_ids, T * topk, num_experts, M_cap, 1, m_indices, row_of, src_of,
-                        reinterpret_cast<uint32_t*>(sa_perm), st)))
-    return r;
-  if (T == 0) return DG_OK;
   QuantArgs p = {};
   p.x = x;
   p.M = T;
@@ -1404,6 +1416,19 @@ int dg_moe_quantize_permute_int8(const int32_t* topk_ids, int T, int topk, int n
   p.topk = topk;
   p.m_indices = m_indices;
   p.src_of = src_of;
+  if (T != 0 && T * topk <= kFewSlots) {
+    p.G = num_experts;
+    p.M_cap = M_cap;
+    p.row_of_out = row_of;
+    if (x_dtype == 0) DG_CUDA_TRY((launch_quantize_permute_few<__nv_bfloat16>(p, di.sms, st)));
+    else DG_CUDA_TRY((launch_quantize_permute_few<float>(p, di.sms, st)));
+    return DG_OK;
+  }
+  // the scales are words of one K group: zero bits are the scale 0 of padding rows
+  if ((r = launch_route(topk_ids, T * topk, num_experts, M_cap, 1, m_indices, row_of, src_of,
+                        reinterpret_cast<uint32_t*>(sa_perm), st)))
+    return r;
+  if (T == 0) return DG_OK;
   if (x_dtype == 0) DG_CUDA_TRY((launch_quantize_int8<__nv_bfloat16, true>(p, st)));
   else DG_CUDA_TRY((launch_quantize_int8<float, true>(p, st)));
   return DG_OK;

@@ -106,6 +106,9 @@ struct QuantArgs {
   int topk;
   int32_t* m_indices;
   int32_t* src_of;
+  // the permuted form of few slots: it routes as well
+  int G, M_cap;
+  int32_t* row_of_out;
 };
 
 // One row a team of W warps (W = blockDim.y warps; blockDim.z teams of one warp
@@ -113,7 +116,7 @@ struct QuantArgs {
 // length, read twice.
 // PERM: every routed slot of the token gets the row's codes.
 template <typename T, int U, bool PERM>
-__global__ void __launch_bounds__(U == 1 ? 512 : 1024) quantize_int8_kernel(const QuantArgs p) {
+__global__ void __launch_bounds__(U == 4 && sizeof(T) == 4 ? 512 : 1024) quantize_int8_kernel(const QuantArgs p) {
   __shared__ uint32_t part[32];
   const int lane = threadIdx.x;
   const int W = blockDim.y;
@@ -127,7 +130,7 @@ __global__ void __launch_bounds__(U == 1 ? 512 : 1024) quantize_int8_kernel(cons
   const int step = 32 * W;
   const int u0 = 32 * warp + lane;
   constexpr int kU = U == 0 ? 1 : U;
-  QuantUnit<T> v[kU];
+  QuantUnit<T> v[kU] = {};
   uint32_t amax = 0;
   if constexpr (U == 0) {
     for (int u = u0; u < units; u += step) {
@@ -142,6 +145,8 @@ __global__ void __launch_bounds__(U == 1 ? 512 : 1024) quantize_int8_kernel(cons
     for (int i = 0; i < U; ++i)
       if (u0 + i * step < units) amax = max(amax, v[i].top());
   }
+  // lane s holds the destination of slot s
+  const int slot_row = PERM && lane < p.topk ? __ldg(p.row_of + row * p.topk + lane) : -1;
   amax = __reduce_max_sync(0xffffffffu, amax);
   if (W > 1) {
     if (lane == 0) part[warp] = amax;
@@ -154,33 +159,187 @@ __global__ void __launch_bounds__(U == 1 ? 512 : 1024) quantize_int8_kernel(cons
     if (warp == 0 && lane == 0) p.scale[row] = scale;
   } else if (warp == 0) {
     for (int s = lane; s < p.topk; s += 32) {
-      const int r = __ldg(p.row_of + row * p.topk + s);
+      const int r = s < 32 ? slot_row : __ldg(p.row_of + row * p.topk + s);
       if (r < 0) continue;
       p.scale[r] = scale;
       p.m_indices[r] = __ldg(p.ids + row * p.topk + s);
       p.src_of[r] = static_cast<int32_t>(row);
     }
   }
-  auto store = [&](int u, const QuantUnit<T>& w) {
-    const uint4 c = int8_codes(w, inverse);
-    if constexpr (PERM) {
-      for (int s = 0; s < p.topk; ++s) {
-        const int r = __ldg(p.row_of + row * p.topk + s);
-        if (r >= 0) *reinterpret_cast<uint4*>(p.q + static_cast<size_t>(r) * p.K + 16 * static_cast<size_t>(u)) = c;
-      }
-    } else {
-      *reinterpret_cast<uint4*>(p.q + static_cast<size_t>(row) * p.K + 16 * static_cast<size_t>(u)) = c;
-    }
-  };
   if constexpr (U == 0) {
-    for (int u = u0; u < units; u += step) {
-      v[0].load(x + 16 * static_cast<size_t>(u));
-      store(u, v[0]);
+    for (int u = u0; u - lane < units; u += step) {
+      const bool in = u < units;
+      if (in) v[0].load(x + 16 * static_cast<size_t>(u));
+      const uint4 c = int8_codes(v[0], inverse);
+      if constexpr (PERM) {
+        for (int s = 0; s < p.topk; ++s) {
+          const int r = s < 32 ? __shfl_sync(0xffffffffu, slot_row, s) : __ldg(p.row_of + row * p.topk + s);
+          if (in && r >= 0) reinterpret_cast<uint4*>(p.q + static_cast<size_t>(r) * p.K)[u] = c;
+        }
+      } else if (in) {
+        reinterpret_cast<uint4*>(p.q + static_cast<size_t>(row) * p.K)[u] = c;
+      }
     }
   } else {
+    uint4 c[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) c[i] = int8_codes(v[i], inverse);
+    for (int s = 0; s < (PERM ? p.topk : 1); ++s) {
+      long long r = row;
+      if constexpr (PERM) r = s < 32 ? __shfl_sync(0xffffffffu, slot_row, s) : __ldg(p.row_of + row * p.topk + s);
+      if (r < 0) continue;
+      uint4* to = reinterpret_cast<uint4*>(p.q + static_cast<size_t>(r) * p.K);
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (u0 + i * step < units) to[u0 + i * step] = c[i];
+    }
+  }
+}
+
+// Routing, quantisation and scattering of few slots (a decode batch) in one
+// launch.  The routing kernel's cluster takes about 8 us whatever the batch
+// (its counting passes, two cluster barriers, a table of 32 counts an expert);
+// here every block counts the experts of all slots and scans the segments for
+// itself, and ranks only its own token's slots among the earlier ones.  Blocks
+// behind the last token only mark padding rows.
+constexpr int kFewSlots = 2048;
+constexpr int kFewThreads = 256;
+
+template <typename T, int U>
+__global__ void __launch_bounds__(kFewThreads) quantize_permute_few_kernel(const QuantArgs p) {
+  __shared__ int id[kFewSlots];
+  __shared__ int count[kMoeMaxExperts];
+  __shared__ int segment[kMoeMaxExperts];
+  __shared__ int slot_row[kFewSlots];
+  __shared__ int part[kFewThreads / 32];
+  __shared__ uint32_t top[kFewThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int t = blockIdx.x;
+  const int n = p.M * p.topk;
+  const int units = p.K / 16;
+  const bool has = t < p.M;
+  grid_dep_wait();
+  grid_dep_launch();
+  // this token's values are on their way while the experts are counted
+  const T* x = static_cast<const T*>(p.x) + static_cast<size_t>(has ? t : 0) * p.K;
+  constexpr int kU = U == 0 ? 1 : U;
+  QuantUnit<T> v[kU] = {};
+  if constexpr (U > 0) {
 #pragma unroll
     for (int i = 0; i < U; ++i)
-      if (u0 + i * step < units) store(u0 + i * step, v[i]);
+      if (has && tid + i * kFewThreads < units) v[i].load(x + 16 * (tid + i * kFewThreads));
+  }
+  for (int e = tid; e < p.G; e += kFewThreads) count[e] = 0;
+  __syncthreads();
+  bool bad = false;
+  for (int i = tid; i < n; i += kFewThreads) {
+    const int e = __ldg(p.ids + i);
+    const bool valid = e >= 0 && e < p.G;
+    bad |= !valid && e != -1;
+    id[i] = valid ? e : -1;
+    if (valid) atomicAdd(&count[e], 1);
+  }
+  if (bad && t == 0) atomicOr(&g_dg_error, 0x2);
+  __syncthreads();
+  // segment offsets: exclusive scan of the counts rounded up to 128, four experts a thread
+  constexpr int kEach = kMoeMaxExperts / kFewThreads;
+  int sum = 0;
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = kEach * tid + i;
+    sum += e < p.G ? (count[e] + 127) & ~127 : 0;
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  if (lane == 31) part[warp] = incl;
+  uint32_t amax = 0;
+  if constexpr (U > 0) {
+#pragma unroll
+    for (int i = 0; i < U; ++i) amax = max(amax, v[i].top());
+  } else if (has) {
+    for (int u = tid; u < units; u += kFewThreads) {
+      v[0].load(x + 16 * static_cast<size_t>(u));
+      amax = max(amax, v[0].top());
+    }
+  }
+  amax = __reduce_max_sync(0xffffffffu, amax);
+  if (lane == 0) top[warp] = amax;
+  __syncthreads();
+  int at = incl - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kFewThreads / 32; ++w) {
+    at += w < warp ? part[w] : 0;
+    total += part[w];
+    amax = max(amax, top[w]);
+  }
+#pragma unroll
+  for (int i = 0; i < kEach; ++i) {
+    const int e = kEach * tid + i;
+    if (e < p.G) {
+      segment[e] = at;
+      at += (count[e] + 127) & ~127;
+    }
+  }
+  __syncthreads();
+  float scale, inverse;
+  int8_scale(amax, scale, inverse);
+  if (has) {
+    // a slot's row: its expert's segment, behind the earlier slots of the same expert
+    for (int s = warp; s < p.topk; s += kFewThreads / 32) {
+      const int pos = t * p.topk + s;
+      const int e = id[pos];
+      int before = 0;
+      for (int i = lane; i < pos; i += 32) before += id[i] == e;
+      before = __reduce_add_sync(0xffffffffu, before);
+      const int r = e < 0 ? -1 : segment[e] + before;
+      if (lane == 0) {
+        slot_row[s] = r;
+        p.row_of_out[pos] = r;
+        if (r >= 0) {
+          p.scale[r] = scale;
+          p.m_indices[r] = e;
+          p.src_of[r] = t;
+        }
+      }
+    }
+    __syncthreads();
+    if constexpr (U > 0) {
+      uint4 c[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) c[i] = int8_codes(v[i], inverse);
+      for (int s = 0; s < p.topk; ++s) {
+        const int r = slot_row[s];
+        if (r < 0) continue;
+        uint4* to = reinterpret_cast<uint4*>(p.q + static_cast<size_t>(r) * p.K);
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+          if (tid + i * kFewThreads < units) to[tid + i * kFewThreads] = c[i];
+      }
+    } else {
+      for (int u = tid; u < units; u += kFewThreads) {
+        v[0].load(x + 16 * static_cast<size_t>(u));
+        const uint4 c = int8_codes(v[0], inverse);
+        for (int s = 0; s < p.topk; ++s)
+          if (slot_row[s] >= 0) reinterpret_cast<uint4*>(p.q + static_cast<size_t>(slot_row[s]) * p.K)[u] = c;
+      }
+    }
+  }
+  // padding rows of the segments, an expert a warp, and the rows behind the last segment
+  const int warps = gridDim.x * (kFewThreads / 32);
+  for (int e = t * (kFewThreads / 32) + warp; e < p.G; e += warps)
+    for (int r = segment[e] + count[e] + lane; r < segment[e] + ((count[e] + 127) & ~127); r += 32) {
+      p.m_indices[r] = -1;
+      p.src_of[r] = -1;
+      p.scale[r] = 0.0f;
+    }
+  for (int r = total + t * kFewThreads + tid; r < p.M_cap; r += gridDim.x * kFewThreads) {
+    p.m_indices[r] = -1;
+    p.src_of[r] = -1;
+    p.scale[r] = 0.0f;
   }
 }
 

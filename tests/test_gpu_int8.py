@@ -301,7 +301,8 @@ def _routing(T, topk, G, seed, drop=0.1):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("T,topk,G,K", [(300, 2, 6, 512), (1, 1, 1, 16), (1, 1, 3, 144), (700, 8, 32, 640),
-                                        (64, 4, 256, 8208), (50, 40, 50, 272), (20, 2, 4, 131056)])
+                                        (64, 4, 256, 8208), (50, 40, 50, 272), (20, 2, 4, 131056), (256, 8, 64, 2064),
+                                        (1, 64, 1024, 512), (255, 8, 1024, 16400), (1100, 2, 9, 7168)])
 def test_quantize_permute_bit_exact(T, topk, G, K, dtype):
     """Into buffers that hold something else first: all that is defined is
     written, and the codes of padding rows are not."""
