@@ -47,7 +47,9 @@ struct Int8Layout {
   static constexpr int kTmemCols = 512;
   static constexpr int kOffB = STAGES * kABytes;
   static constexpr int kOffEpi = kOffB + STAGES * kBBytes;
-  static constexpr int kOffBar = kOffEpi + 8 * kEpiBuf;
+  static constexpr int kMine = (BN / 32 + 1) / 2;  // 32-column chunks of an epilogue warp (the second one's may be one less)
+  static constexpr int kOffScale = kOffEpi + 8 * kEpiBuf;  // B's scales of each epilogue warp's chunks
+  static constexpr int kOffBar = kOffScale + 8 * kMine * 32 * 4;
   static constexpr int kNumBars = 2 * STAGES + 2 * 2 + 1;
   static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kOffGroups = kOffMisc + 16;
@@ -232,8 +234,9 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     const int half = epi >> 2;
     uint8_t* buf = smem + L::kOffEpi + epi * L::kEpiBuf;
     const uint32_t empty0 = kPair ? mapa_shared(smem_u32(tmem_empty), 0) : smem_u32(tmem_empty);
+    float* sbuf = reinterpret_cast<float*>(smem + L::kOffScale) + epi * L::kMine * 32;
     constexpr int kChunks = BN / 32;
-    constexpr int kMine = (kChunks + 1) / 2;  // of the first warp; an odd last chunk is its own
+    constexpr int kMine = L::kMine;
     uint32_t own = 0;
     for (int t = unit0; t < ntiles; t += units) {
       const Tile tl = tile_of<MODE, L::kTileM>(t, p, prefix, counts);
@@ -268,7 +271,14 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
       const int zd = MODE == MODE_MASKED ? tl.g : 0;
       const size_t row_g = static_cast<size_t>(zd) * p.rows + m;
       const float sa = valid ? __ldg(p.sa + row_g) : 0.0f;
+      // B's scales of the warp's chunks come in while the tile is computed
       const float* sb = p.sb + static_cast<size_t>(expert) * p.N;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int col = n0 + 32 * (half + 2 * i) + lane;
+        sbuf[32 * i + lane] = col < p.N ? __ldg(sb + col) : 0.0f;
+      }
+      __syncwarp();
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * L::kAccStride;
 
       bool ok = wait_phase<false>(&tmem_full[acc], use & 1, abort_flag, p.wait_limit_ns);
@@ -296,11 +306,10 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
             if (col + per16 * i < p.N) static_cast<uint4*>(d_row)[i] = w[i];
         }
       };
-      auto finish = [&](uint32_t (&r)[32], int col0) {
+      auto finish = [&](uint32_t (&r)[32], int col0, const float* scales) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 b = col0 + 4 * i < p.N ? __ldg(reinterpret_cast<const float4*>(sb + col0) + i)
-                                              : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float4 b = reinterpret_cast<const float4*>(scales)[i];
           r[4 * i] = __float_as_uint(__int2float_rn(static_cast<int>(r[4 * i])) * sa * b.x);
           r[4 * i + 1] = __float_as_uint(__int2float_rn(static_cast<int>(r[4 * i + 1])) * sa * b.y);
           r[4 * i + 2] = __float_as_uint(__int2float_rn(static_cast<int>(r[4 * i + 2])) * sa * b.z);
@@ -333,25 +342,31 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         }
       };
 
-      if (any_valid) {
-        uint32_t r[2][32];
-        if (n0 + 32 * half < p.N) tmem_ld_32x32b_x32(t_row + 32 * half, r[0]);
-        tmem_wait_ld();
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int c = half + 2 * i;
-          const int col0 = n0 + 32 * c;
-          if (c >= kChunks || col0 >= p.N) break;
-          if (c + 2 < kChunks && col0 + 64 < p.N) tmem_ld_32x32b_x32(t_row + 32 * (c + 2), r[(i + 1) & 1]);
-          finish(r[i & 1], col0);
-          tmem_wait_ld();
+      // The accumulator is handed back as soon as its last chunk has been read.
+      auto release = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if constexpr (kPair) mbar_arrive_remote(empty0 + 8 * acc);
+          else mbar_arrive(&tmem_empty[acc]);
         }
+      };
+      const int mine = any_valid ? min(kMine, max(0, (min(kChunks, (p.N - n0 + 31) / 32) - half + 1) / 2)) : 0;
+      if (mine == 0) {
+        release();
+        continue;
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) {
-        if constexpr (kPair) mbar_arrive_remote(empty0 + 8 * acc);
-        else mbar_arrive(&tmem_empty[acc]);
+      uint32_t r[2][32];
+      tmem_ld_32x32b_x32(t_row + 32 * half, r[0]);
+      tmem_wait_ld();
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        if (i >= mine) break;
+        const int c = half + 2 * i;
+        if (i + 1 < mine) tmem_ld_32x32b_x32(t_row + 32 * (c + 2), r[(i + 1) & 1]);
+        else release();
+        finish(r[i & 1], n0 + 32 * c, sbuf + 32 * i);
+        if (i + 1 < mine) tmem_wait_ld();
       }
     }
     // the staging buffers must have been read before the CTA exits
