@@ -217,11 +217,15 @@ __device__ __forceinline__ uint32_t pack_scale_word(const float* row, int kp, in
 // (another role gave up) or this wait exceeded its limit (sets the error word).
 // A plain try_wait may keep the thread suspended until the phase completes,
 // so every probe here carries a suspend-time hint (kPollNs): the loop looks
-// at the clock and the abort flag at least that often.
+// at the clock and the abort flag at least that often.  The clock is read
+// only when the first probe fails: reading it takes longer than a wait that is
+// already satisfied.
 constexpr uint32_t kPollNs = 1000;
 template <bool kCluster>
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                            uint64_t limit_ns) {
+  if (kCluster ? mbar_try_wait_cluster_hint(bar, parity, kPollNs) : mbar_try_wait_hint(bar, parity, kPollNs))
+    return true;
   const uint64_t t0 = global_timer_ns();
   while (true) {
     if (kCluster ? mbar_try_wait_cluster_hint(bar, parity, kPollNs) : mbar_try_wait_hint(bar, parity, kPollNs))
@@ -237,6 +241,7 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
 
 // Wait used while draining at exit: ignores the abort flag, still bounded.
 __device__ __forceinline__ void wait_phase_drain(uint64_t* bar, uint32_t parity) {
+  if (mbar_try_wait_hint(bar, parity, kPollNs)) return;
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait_hint(bar, parity, kPollNs)) {
     if (global_timer_ns() - t0 > kWaitLimitNs) {

@@ -79,6 +79,8 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + L::kOffMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kOffMisc + 4);
   uint32_t* peer_loads = reinterpret_cast<uint32_t*>(smem + L::kOffMisc + 8);  // written by the pair's second CTA
+  // pairs: the issuer has waited for every load of both CTAs (written in both by the first)
+  volatile uint32_t* all_landed = reinterpret_cast<volatile uint32_t*>(smem + L::kOffMisc + 12);
   int* prefix = reinterpret_cast<int*>(smem + L::kOffGroups);
   int* counts = prefix + kMaxMaskedGroups + 1;
   uint32_t it = 0;  // loads issued (producer warp)
@@ -102,6 +104,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     }
     mbar_init(final_bar, 1);
     *abort_flag = 0;
+    *all_landed = 0;
     fence_barrier_init();
     prefetch_tensormap(&tm_a);
     prefetch_tensormap(&tm_b);
@@ -195,25 +198,31 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * L::kAccStride;
+        // An instruction of the tensor core costs this thread some 60 cycles to
+        // issue, a K block 300 of the 512 that it takes on 256 columns: so the
+        // rest is kept short, and the next block's barrier is looked at between
+        // the MMAs of this one.
         uint32_t accumulate = 0;
+        bool ready = mbar_test_wait_addr(full_base + 8 * s, phase);
         for (int kb = 0; kb < num_kb; ++kb) {
-          if (!mbar_try_wait_addr(full_base + 8 * s, phase)) {
+          if (!ready && !mbar_try_wait_addr(full_base + 8 * s, phase)) {
             ok = wait_phase<false>(&full_bar[s], phase, abort_flag, p.wait_limit_ns);
             if (!ok) break;
           }
-          tc_fence_after();
           const uint64_t a = a0 + s * (L::kABytes >> 4), b = b0 + s * (L::kBBytes >> 4);
+          const uint32_t done = empty_base + 8 * s;
           mma_i8<CTAS>(d_tmem, a, b, idesc, accumulate);
           mma_i8<CTAS>(d_tmem, a + 2, b + 2, idesc, 1u);
-          mma_i8<CTAS>(d_tmem, a + 4, b + 4, idesc, 1u);
-          mma_i8<CTAS>(d_tmem, a + 6, b + 6, idesc, 1u);
-          accumulate = 1;
-          if constexpr (kPair) tc_commit_pair_addr(empty_base + 8 * s);
-          else tc_commit_addr<1>(empty_base + 8 * s);
           if (++s == STAGES) {
             s = 0;
             phase ^= 1;
           }
+          ready = mbar_test_wait_addr(full_base + 8 * s, phase);
+          mma_i8<CTAS>(d_tmem, a + 4, b + 4, idesc, 1u);
+          mma_i8<CTAS>(d_tmem, a + 6, b + 6, idesc, 1u);
+          accumulate = 1;
+          if constexpr (kPair) tc_commit_pair_addr(done);
+          else tc_commit_addr<1>(done);
         }
         if (!ok) break;
         if constexpr (kPair) tc_commit_pair(&tmem_full[acc]);
@@ -222,6 +231,13 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
       // all MMAs issued here complete before TMEM is freed
       tc_commit<CTAS>(final_bar);
       wait_phase_drain(final_bar, 0);
+      if constexpr (kPair) {
+        if (ok) {
+          const uint32_t at = smem_u32(const_cast<uint32_t*>(all_landed));
+          st_shared_cluster_u32(mapa_shared(at, 0), 1);
+          st_shared_cluster_u32(mapa_shared(at, 1), 1);
+        }
+      }
     }
     __syncwarp();
   } else {
@@ -378,20 +394,22 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   tc_fence_before();
   if constexpr (kPair) {
     cluster_sync();  // both CTAs have stopped issuing; the second CTA's load count is visible
-    if (rank == 0 && warp == 1 && lane == 0) {
-      // A CTA that gave up before issuing load j never arrives: arrive in its
-      // place, then wait for the loads that were issued.
-      const uint32_t it1 = *reinterpret_cast<volatile uint32_t*>(peer_loads);
-      const uint32_t hi = it > it1 ? it : it1;
-      for (uint32_t j = hi > STAGES ? hi - STAGES : 0; j < hi; ++j) {
-        uint64_t* b = &full_bar[j % STAGES];
-        if (j >= it) mbar_arrive(b);
-        if (j >= it1) mbar_arrive(b);
-        wait_phase_drain(b, (j / STAGES) & 1);
+    if (!*all_landed) {
+      if (rank == 0 && warp == 1 && lane == 0) {
+        // A CTA that gave up before issuing load j never arrives: arrive in its
+        // place, then wait for the loads that were issued.
+        const uint32_t it1 = *reinterpret_cast<volatile uint32_t*>(peer_loads);
+        const uint32_t hi = it > it1 ? it : it1;
+        for (uint32_t j = hi > STAGES ? hi - STAGES : 0; j < hi; ++j) {
+          uint64_t* b = &full_bar[j % STAGES];
+          if (j >= it) mbar_arrive(b);
+          if (j >= it1) mbar_arrive(b);
+          wait_phase_drain(b, (j / STAGES) & 1);
+        }
       }
+      __syncwarp();
+      cluster_sync();
     }
-    __syncwarp();
-    cluster_sync();
   } else {
     __syncthreads();
   }
