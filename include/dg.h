@@ -376,13 +376,15 @@ int dg_set_pdl(int enable);
  *   contiguous          : (128|224|256, 1, 1), (224, 2, 2)
  *   FP32 output (_ex)   : (128|224|256, 1, 1)
  *   NN / TN / TT        : fewer tiles.
+ *   int8, all layouts   : (64|128|256, 1, 1), (128|256, 2, 1)
  * The triple must be built for at least one entry point (else
  * DG_ERR_UNSUPPORTED).  An entry point that does not build it keeps the
  * heuristic's choice. */
 int dg_set_config(int block_n, int ctas, int pipes);
 
 /* Describes the configuration the heuristic picks for a problem, as
- * "BMxBNxSTAGES[(2cta)]/grid" in buf (kind: 0 dense, 1 contiguous, 2 masked). */
+ * "BMxBNxSTAGES[(2cta)]/grid" in buf (kind: 0 dense, 1 contiguous, 2 masked;
+ * 3, 4, 5 the same for the int8 products). */
 int dg_describe_config(int kind, int M, int N, int K, int num_groups, char* buf, int buflen);
 
 /* Text of the last host-side error on this thread ("" if none). */

@@ -643,7 +643,7 @@ def set_config(block_n: int, ctas: int = 0, pipes: int = 0) -> None:
 
 def describe_config(kind: str, M: int, N: int, K: int, num_groups: int = 1) -> str:
     buf = ctypes.create_string_buffer(64)
-    k = {"dense": 0, "contiguous": 1, "masked": 2}[kind]
+    k = {"dense": 0, "contiguous": 1, "masked": 2, "int8_dense": 3, "int8_contiguous": 4, "int8_masked": 5}[kind]
     _check(load().dg_describe_config(k, M, N, K, num_groups, buf, 64))
     return buf.value.decode()
 

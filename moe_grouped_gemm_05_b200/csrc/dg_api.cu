@@ -652,18 +652,28 @@ static const Config* int8_config_table(int* count) {
   static const Config table[] = {
       make_int8_config<64, 8, mode, 1, f32>(), make_int8_config<128, 6, mode, 1, f32>(),
       make_int8_config<256, 4, mode, 1, f32>(), make_int8_config<128, 8, mode, 2, f32>(),
-      make_int8_config<256, 6, mode, 2, f32>(), make_int8_config<224, 6, mode, 2, f32>(),
+      make_int8_config<256, 6, mode, 2, f32>(),
   };
   *count = static_cast<int>(sizeof(table) / sizeof(table[0]));
   return table;
 }
 
 // Time of one 128-wide K block of a tile and of the rest of a tile, in ns, as
-// in the FP8 kernels' cost model.
+// in the FP8 kernels' cost model: fitted to 4096x7168x2048 and to contiguous 8 x
+// (512 rows x 4096 x 7168), back to back.
 static const CostParams kCostInt8[] = {
-    {64, 1, 1, false, 200, 600},  {128, 1, 1, false, 210, 750},   {256, 1, 1, false, 330, 1300},
-    {128, 2, 1, false, 220, 900}, {256, 2, 1, false, 310, 1500}, {224, 2, 1, false, 271, 1400},
+    {64, 1, 1, false, 265, 600},  {128, 1, 1, false, 290, 700},   {256, 1, 1, false, 430, 700},
+    {128, 2, 1, false, 285, 750}, {256, 2, 1, false, 385, 800},
 };
+
+// Whether an int8 product is built with this tile (every mode builds the same).
+static bool find_int8_config(int bn, int ctas, int pipes) {
+  int n = 0;
+  const Config* t = int8_config_table<MODE_DENSE>(&n);
+  for (int i = 0; i < n; ++i)
+    if (t[i].bn == bn && (ctas == 0 || t[i].ctas == ctas) && pipes <= 1) return true;
+  return false;
+}
 
 template <int MODE>
 static const Config* choose_int8_config(long long rows_est, int N, int K, int sms, int groups) {
@@ -691,7 +701,8 @@ static const Config* choose_int8_config(long long rows_est, int N, int K, int sm
       m_tiles = static_cast<long long>(groups) * ((per + tile_m - 1) / tile_m);
     } else {
       m_tiles = (rows_est + tile_m - 1) / tile_m;
-      if (mode == MODE_CONTIG && c.ctas == 2) m_tiles += (groups + 1) / 2;
+      // a run of blocks of odd length, every other expert's, ends in a half-empty pair
+      if (mode == MODE_CONTIG && c.ctas == 2) m_tiles += (groups + 3) / 4;
     }
     const long long n_tiles = (N + c.bn - 1) / c.bn;
     const long long units = std::max(1, sms / c.ctas);
@@ -1010,7 +1021,7 @@ int dg_set_config(int block_n, int ctas, int pipes) {
   if (!find_config<MODE_DENSE>(block_n, ctas, pipes) && !find_config<MODE_CONTIG>(block_n, ctas, pipes) &&
       !find_config<MODE_MASKED>(block_n, ctas, pipes) && !find_config<MODE_DENSE_F32>(block_n, ctas, pipes) &&
       !find_config<MODE_DENSE_MN>(block_n, ctas, pipes) && !find_config<MODE_DENSE_MN + 1>(block_n, ctas, pipes) &&
-      !find_config<MODE_DENSE_MN + 2>(block_n, ctas, pipes))
+      !find_config<MODE_DENSE_MN + 2>(block_n, ctas, pipes) && !find_int8_config(block_n, ctas, pipes))
     return fail(DG_ERR_UNSUPPORTED, "block_n=%d with ctas=%d, pipes=%d is not built", block_n, ctas, pipes);
   t_force_bn = block_n;
   t_force_ctas = ctas;
@@ -1028,7 +1039,15 @@ int dg_describe_config(int kind, int M, int N, int K, int num_groups, char* buf,
   if (N <= 0 || K <= 0) return fail(DG_ERR_SHAPE, "N and K must be positive");
   const Config* c = nullptr;
   long long tiles = 0;
-  if (kind == 2) {
+  if (kind >= 3 && kind <= 5) {  // the int8 products
+    const long long est = kind == 5 ? std::max<long long>(1, static_cast<long long>(num_groups) * M / 2) : M;
+    c = kind == 3   ? choose_int8_config<MODE_DENSE>(est, N, K, sms, 1)
+        : kind == 4 ? choose_int8_config<MODE_CONTIG>(est, N, K, sms, num_groups)
+                    : choose_int8_config<MODE_MASKED>(est, N, K, sms, num_groups);
+    if (c)
+      tiles = static_cast<long long>(kind == 5 ? num_groups : 1) * ((M + 128 * c->ctas - 1) / (128 * c->ctas)) *
+              ((N + c->bn - 1) / c->bn);
+  } else if (kind == 2) {
     const long long est = std::max<long long>(1, static_cast<long long>(num_groups) * M / 2);
     c = choose_config<MODE_MASKED>(est, N, K, sms, num_groups, M);
     if (c) tiles = static_cast<long long>(num_groups) * ((M + 128 * c->ctas - 1) / (128 * c->ctas)) * ((N + c->bn - 1) / c->bn);

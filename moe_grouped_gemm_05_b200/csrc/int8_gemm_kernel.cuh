@@ -47,7 +47,7 @@ struct Int8Layout {
   static constexpr int kTmemCols = 512;
   static constexpr int kOffB = STAGES * kABytes;
   static constexpr int kOffEpi = kOffB + STAGES * kBBytes;
-  static constexpr int kMine = (BN / 32 + 1) / 2;  // 32-column chunks of an epilogue warp (the second one's may be one less)
+  static constexpr int kMine = BN / 64;  // 32-column chunks of an epilogue warp
   static constexpr int kOffScale = kOffEpi + 8 * kEpiBuf;  // B's scales of each epilogue warp's chunks
   static constexpr int kOffBar = kOffScale + 8 * kMine * 32 * 4;
   static constexpr int kNumBars = 2 * STAGES + 2 * 2 + 1;
@@ -58,7 +58,7 @@ struct Int8Layout {
                                                                            : 0;
   static constexpr int kSmemBytes = kOffGroups + kGroupsBytes + 1024;
   static_assert(kSmemBytes <= kMaxSmem, "shared-memory budget exceeded");
-  static_assert(BN % 32 == 0 && BN <= 256 && 2 * kAccStride <= kTmemCols, "two accumulators fit in tensor memory");
+  static_assert(BN % 64 == 0 && BN <= 256 && 2 * kAccStride <= kTmemCols, "two accumulators fit in tensor memory");
   static_assert(kOffEpi % 1024 == 0 && kBBytes % 1024 == 0, "swizzle atoms are 1024-byte aligned");
 };
 
@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
       }
     } else if (rank == 1 && lane == 0) {
       st_shared_cluster_u32(mapa_shared(smem_u32(peer_loads), 0), it);
+      fence_cluster();
     }
     __syncwarp();
   } else if (warp == 0) {
@@ -236,6 +237,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
           const uint32_t at = smem_u32(const_cast<uint32_t*>(all_landed));
           st_shared_cluster_u32(mapa_shared(at, 0), 1);
           st_shared_cluster_u32(mapa_shared(at, 1), 1);
+          fence_cluster();
         }
       }
     }
@@ -251,7 +253,6 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     uint8_t* buf = smem + L::kOffEpi + epi * L::kEpiBuf;
     const uint32_t empty0 = kPair ? mapa_shared(smem_u32(tmem_empty), 0) : smem_u32(tmem_empty);
     float* sbuf = reinterpret_cast<float*>(smem + L::kOffScale) + epi * L::kMine * 32;
-    constexpr int kChunks = BN / 32;
     constexpr int kMine = L::kMine;
     uint32_t own = 0;
     for (int t = unit0; t < ntiles; t += units) {
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
           else mbar_arrive(&tmem_empty[acc]);
         }
       };
-      const int mine = any_valid ? min(kMine, max(0, (min(kChunks, (p.N - n0 + 31) / 32) - half + 1) / 2)) : 0;
+      const int mine = any_valid ? min(kMine, max(0, ((p.N - n0 + 31) / 32 - half + 1) / 2)) : 0;
       if (mine == 0) {
         release();
         continue;
@@ -393,7 +394,9 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   // ---------------------------------------------------------------- teardown
   tc_fence_before();
   if constexpr (kPair) {
-    cluster_sync();  // both CTAs have stopped issuing; the second CTA's load count is visible
+    // Both CTAs have stopped issuing, and what they left for one another is
+    // visible; the epilogue's global stores need not be waited for.
+    cluster_sync_relaxed();
     if (!*all_landed) {
       if (rank == 0 && warp == 1 && lane == 0) {
         // A CTA that gave up before issuing load j never arrives: arrive in its
