@@ -32,7 +32,7 @@ namespace dg {
 
 constexpr int kGateMaxTopk = 32;    // lane j of the team holds slot j
 constexpr int kGateMaxGroups = 32;  // lane g holds group g
-constexpr int kGateWarps = 4;       // warps of a block
+constexpr int kGateWarps = 4;       // warps of a block (8 and 16 measured the same)
 constexpr int kGateList = 32;       // listed experts of a token that are ranked at once
 
 struct GateArgs {
@@ -252,6 +252,20 @@ __device__ __forceinline__ float fast_rcp(float x) {
   return r;
 }
 constexpr float kLog2e = 1.4426950408889634f;
+
+// n += (x >= bound); and, where x >= bound, (x, e) to the shared list at `to`,
+// which moves on.  Written out, since the compiler makes branches of them.
+__device__ __forceinline__ void count_from(int& n, float x, float bound) {
+  asm("{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %1, %2;\n\t@p add.s32 %0, %0, 1;\n\t}" : "+r"(n) : "f"(x), "f"(bound));
+}
+__device__ __forceinline__ void list_from(uint32_t& to, float x, int e, float bound) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ge.f32 p, %1, %3;\n\t@p st.shared.v2.b32 [%0], {%1, %2};\n\t"
+      "@p add.u32 %0, %0, 8;\n\t}"
+      : "+r"(to)
+      : "f"(x), "r"(e), "f"(bound)
+      : "memory");
+}
 
 // The two largest of {a1 >= a2} and {b1 >= b2}, in a1 >= a2.
 template <typename R>
@@ -588,12 +602,11 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
   const float bound = kth == -INFINITY ? -FLT_MAX : BIAS ? kth - near : kth;
   int n = 0;
 #pragma unroll
-  for (int i = 0; i < V; ++i) n += c[i] >= bound;
+  for (int i = 0; i < V; ++i) count_from(n, c[i], bound);
   __syncwarp();
-  int pos = n > 0 ? atomicAdd(count, n) : 0;
+  uint32_t to = smem_u32(list) + 8 * (n > 0 ? atomicAdd(count, n) : 0);
 #pragma unroll
-  for (int i = 0; i < V; ++i)
-    if (c[i] >= bound) list[pos++] = make_float2(c[i], __int_as_float(tl * V + i));
+  for (int i = 0; i < V; ++i) list_from(to, c[i], tl * V + i, bound);
   __syncwarp();
   const int all = *count;
   const int m = min(all, kGateList);
