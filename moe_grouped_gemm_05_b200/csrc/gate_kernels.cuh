@@ -685,6 +685,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
     // shows whether the last place was a close one
     const int rounds = BIAS ? p.topk + 1 : p.topk;
     float before = INFINITY;
+    int before_e = -1;
     bool close = false;
     int found_id = -1;
     for (int j = 0; j < rounds; ++j) {
@@ -692,8 +693,6 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
 #pragma unroll
       for (int i = 1; i < V; ++i) lead = fmaxf(lead, c[i]);
       const float next = team_max<L>(lead);
-      close |= BIAS && next > -INFINITY && before - next <= near;
-      before = next;
       const uint32_t who = __ballot_sync(0xffffffffu, lead == next && next > -INFINITY) >> (lane & ~(L - 1));
       const int src = __ffs(L == 32 ? who : who & ((1u << (L & 31)) - 1u)) - 1;  // -1: none is left
       int e = -1;
@@ -708,6 +707,12 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
           }
       }
       e = __shfl_sync(0xffffffffu, e, src < 0 ? 0 : src, L);
+      // equal logits with equal biases tie whatever the precision
+      if (BIAS && src >= 0 && before - next <= near &&
+          !(gate_at(row, e) == gate_at(row, before_e) && __ldg(p.bias + e) == __ldg(p.bias + before_e)))
+        close = true;
+      before = next;
+      before_e = e;
       if (tl == j && j < p.topk && src >= 0) found_id = e;
     }
     if (all > kGateList) {
