@@ -15,8 +15,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libdg.so")
 SOURCES = ["dg_api.cu"]
-DEPS = ["dg_api.cu", "fp8_gemm_kernel.cuh", "int8_gemm_kernel.cuh", "ptx.cuh", "quant_kernel.cuh",
-        "int8_quant_kernel.cuh", "moe_kernels.cuh", "gate_kernels.cuh"]
+DEPS = ["dg_api.cu", "fp8_gemm_kernel.cuh", "int8_gemm_kernel.cuh", "ptx.cuh", "int8_ptx.cuh",
+        "quant_kernel.cuh", "int8_quant_kernel.cuh", "moe_kernels.cuh", "gate_kernels.cuh"]
 
 
 def nvcc_path() -> str:

@@ -217,15 +217,11 @@ __device__ __forceinline__ uint32_t pack_scale_word(const float* row, int kp, in
 // (another role gave up) or this wait exceeded its limit (sets the error word).
 // A plain try_wait may keep the thread suspended until the phase completes,
 // so every probe here carries a suspend-time hint (kPollNs): the loop looks
-// at the clock and the abort flag at least that often.  The clock is read
-// only when the first probe fails: reading it takes longer than a wait that is
-// already satisfied.
+// at the clock and the abort flag at least that often.
 constexpr uint32_t kPollNs = 1000;
 template <bool kCluster>
 __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                            uint64_t limit_ns) {
-  if (kCluster ? mbar_try_wait_cluster_hint(bar, parity, kPollNs) : mbar_try_wait_hint(bar, parity, kPollNs))
-    return true;
   const uint64_t t0 = global_timer_ns();
   while (true) {
     if (kCluster ? mbar_try_wait_cluster_hint(bar, parity, kPollNs) : mbar_try_wait_hint(bar, parity, kPollNs))
@@ -241,7 +237,6 @@ __device__ __forceinline__ bool wait_phase(uint64_t* bar, uint32_t parity, volat
 
 // Wait used while draining at exit: ignores the abort flag, still bounded.
 __device__ __forceinline__ void wait_phase_drain(uint64_t* bar, uint32_t parity) {
-  if (mbar_try_wait_hint(bar, parity, kPollNs)) return;
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait_hint(bar, parity, kPollNs)) {
     if (global_timer_ns() - t0 > kWaitLimitNs) {
@@ -329,75 +324,6 @@ __device__ __forceinline__ int contig_expert(const Tile& tl, const GemmArgs& p) 
   return e;
 }
 
-// One warp: the masked layout's valid rows per expert and running sum of tiles.
-template <int TILE_M>
-__device__ __forceinline__ void masked_tile_prefix(const GemmArgs& p, int* prefix, int* counts, int lane) {
-  // counts[g] = clamp(masked_m[g], 0, M_max); prefix = running sum of tiles
-  int run = 0;
-  for (int base = 0; base < p.G; base += 32) {
-    const int g = base + lane;
-    int tiles = 0;
-    if (g < p.G) {
-      int mg = __ldg(&p.masked_m[g]);
-      if (mg < 0 || mg > p.rows) {
-        if (blockIdx.x == 0) atomicOr(&g_dg_error, 0x4);
-        mg = mg < 0 ? 0 : p.rows;
-      }
-      counts[g] = mg;
-      tiles = ((mg + TILE_M - 1) / TILE_M) * p.num_n_blocks;
-    }
-    int incl = tiles;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    if (g < p.G) prefix[g + 1] = run + incl;
-    run += __shfl_sync(0xffffffffu, incl, 31);
-  }
-  if (lane == 0) prefix[0] = 0;
-}
-
-// One warp: the contiguous layout's pair table (count, then first blocks).
-__device__ __forceinline__ void contig_pair_table(const GemmArgs& p, int* prefix, int lane) {
-  // Pair table: block b (128 rows, expert = that of its first row) starts a
-  // pair when it lies an even number of blocks into its run of equal
-  // experts; blocks with an index outside [0, G) start none.  The experts
-  // of all blocks are loaded at once (at most 32 per lane), then scanned.
-  const int nb = p.rows / 128;
-  int ev[kMaxContigBlocks / 32];
-#pragma unroll
-  for (int i = 0; i < kMaxContigBlocks / 32; ++i) {
-    const int b = 32 * i + lane;
-    ev[i] = b < nb ? __ldg(&p.m_indices[b * 128]) : -1;
-  }
-  int count = 0, run_start = 0, prev_e = -2;
-#pragma unroll
-  for (int i = 0; i < kMaxContigBlocks / 32; ++i) {
-    if (32 * i >= nb) break;
-    const int b = 32 * i + lane;
-    const int e = ev[i];
-    if (b < nb && (e < -1 || e >= p.G) && blockIdx.x == 0) atomicOr(&g_dg_error, 0x2);
-    int e_prev = __shfl_up_sync(0xffffffffu, e, 1);
-    if (lane == 0) e_prev = prev_e;
-    // start of the run holding block b: the last block <= b where the expert changes
-    int rs = (b < nb && (b == 0 || e != e_prev)) ? b : -1;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, rs, o);
-      if (lane >= o) rs = max(rs, v);
-    }
-    if (rs < 0) rs = run_start;
-    const bool starts = b < nb && e >= 0 && e < p.G && ((b - rs) & 1) == 0;
-    const uint32_t bal = __ballot_sync(0xffffffffu, starts);
-    if (starts) prefix[1 + count + __popc(bal & ((1u << lane) - 1u))] = b;
-    count += __popc(bal);
-    run_start = __shfl_sync(0xffffffffu, rs, 31);
-    prev_e = __shfl_sync(0xffffffffu, e, 31);
-  }
-  if (lane == 0) prefix[0] = count;
-}
-
 template <int BN, int STAGES, int MODE, int CTAS, bool OUT_F32 = false, int PIPES = 1, int LAYOUT = 0,
           bool SPLITK = false, int A_ROWS = 128>
 __global__ void __launch_bounds__(kThreadsFor<PIPES>, 1)
@@ -479,8 +405,70 @@ __global__ void __launch_bounds__(kThreadsFor<PIPES>, 1)
   // grid's tail; from here on its results are visible.
   grid_dep_wait();
   grid_dep_launch();
-  if (MODE == MODE_MASKED && warp == kEpi0) masked_tile_prefix<L::kTileM>(p, prefix, counts, lane);
-  if (MODE == MODE_CONTIG && kPair && warp == kEpi0) contig_pair_table(p, prefix, lane);
+  if (MODE == MODE_MASKED && warp == kEpi0) {
+    // counts[g] = clamp(masked_m[g], 0, M_max); prefix = running sum of tiles
+    int run = 0;
+    for (int base = 0; base < p.G; base += 32) {
+      const int g = base + lane;
+      int tiles = 0;
+      if (g < p.G) {
+        int mg = __ldg(&p.masked_m[g]);
+        if (mg < 0 || mg > p.rows) {
+          if (blockIdx.x == 0) atomicOr(&g_dg_error, 0x4);
+          mg = mg < 0 ? 0 : p.rows;
+        }
+        counts[g] = mg;
+        tiles = ((mg + L::kTileM - 1) / L::kTileM) * p.num_n_blocks;
+      }
+      int incl = tiles;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (g < p.G) prefix[g + 1] = run + incl;
+      run += __shfl_sync(0xffffffffu, incl, 31);
+    }
+    if (lane == 0) prefix[0] = 0;
+  }
+  if (MODE == MODE_CONTIG && kPair && warp == kEpi0) {
+    // Pair table: block b (128 rows, expert = that of its first row) starts a
+    // pair when it lies an even number of blocks into its run of equal
+    // experts; blocks with an index outside [0, G) start none.  The experts
+    // of all blocks are loaded at once (at most 32 per lane), then scanned.
+    const int nb = p.rows / 128;
+    int ev[kMaxContigBlocks / 32];
+#pragma unroll
+    for (int i = 0; i < kMaxContigBlocks / 32; ++i) {
+      const int b = 32 * i + lane;
+      ev[i] = b < nb ? __ldg(&p.m_indices[b * 128]) : -1;
+    }
+    int count = 0, run_start = 0, prev_e = -2;
+#pragma unroll
+    for (int i = 0; i < kMaxContigBlocks / 32; ++i) {
+      if (32 * i >= nb) break;
+      const int b = 32 * i + lane;
+      const int e = ev[i];
+      if (b < nb && (e < -1 || e >= p.G) && blockIdx.x == 0) atomicOr(&g_dg_error, 0x2);
+      int e_prev = __shfl_up_sync(0xffffffffu, e, 1);
+      if (lane == 0) e_prev = prev_e;
+      // start of the run holding block b: the last block <= b where the expert changes
+      int rs = (b < nb && (b == 0 || e != e_prev)) ? b : -1;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, rs, o);
+        if (lane >= o) rs = max(rs, v);
+      }
+      if (rs < 0) rs = run_start;
+      const bool starts = b < nb && e >= 0 && e < p.G && ((b - rs) & 1) == 0;
+      const uint32_t bal = __ballot_sync(0xffffffffu, starts);
+      if (starts) prefix[1 + count + __popc(bal & ((1u << lane) - 1u))] = b;
+      count += __popc(bal);
+      run_start = __shfl_sync(0xffffffffu, rs, 31);
+      prev_e = __shfl_sync(0xffffffffu, e, 31);
+    }
+    if (lane == 0) prefix[0] = count;
+  }
   tc_fence_before();
   if constexpr (kPair) cluster_sync(); else __syncthreads();
   tc_fence_after();

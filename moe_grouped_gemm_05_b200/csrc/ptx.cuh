@@ -78,19 +78,6 @@ __device__ __forceinline__ bool mbar_try_wait_addr(uint32_t bar, uint32_t parity
   return ok != 0;
 }
 
-// Whether the phase is complete, without waiting for it.
-__device__ __forceinline__ bool mbar_test_wait_addr(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 __device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -184,15 +171,7 @@ __device__ __forceinline__ void cluster_sync() {
                    : "memory");
 }
 
-// Same without the release: for threads that have published nothing, or have
-// fenced what they did.
-__device__ __forceinline__ void cluster_sync_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
 // ----------------------------------------------------------------- fences
-
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 
 __device__ __forceinline__ void fence_proxy_async_smem() {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -358,26 +337,6 @@ __device__ __forceinline__ void mma_mxf8f6f4(uint32_t d_tmem, uint64_t a_desc, u
         : "memory");
 }
 
-// D(tmem) (+)= A . B^T, int8 x int8 into int32, one K=32 step.
-template <int CG>
-__device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
-  if constexpr (CG == 1)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-        : "memory");
-}
-
 // Copies 32 rows x 128 bits from shared memory into TMEM columns [taddr, taddr+4),
 // replicated into all four 32-lane quarters (with CG == 2: in both CTAs, each from
 // its own shared memory).
@@ -462,14 +421,6 @@ __host__ __device__ constexpr uint32_t make_idesc_mxf8(uint32_t M, uint32_t N, u
          | (1u << 23)                // scale type UE8M0
          | ((M >> 4) << 24)          // M / 16
          | ((sfa_id & 3u) << 29);    // A scale-factor byte selector
-}
-
-// Instruction descriptor of kind::i8: signed 8-bit A and B (both K-major),
-// int32 accumulators that wrap (no saturation), MMA shape M x N.
-__host__ __device__ constexpr uint32_t make_idesc_i8(uint32_t M, uint32_t N) {
-  return (2u << 4)                   // D format: S32
-         | (1u << 7) | (1u << 10)    // A, B formats: signed 8 bits
-         | ((N >> 3) << 17) | ((M >> 4) << 24);
 }
 
 }  // namespace dg
