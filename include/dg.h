@@ -376,7 +376,7 @@ int dg_set_pdl(int enable);
  *   contiguous          : (128|224|256, 1, 1), (224, 2, 2)
  *   FP32 output (_ex)   : (128|224|256, 1, 1)
  *   NN / TN / TT        : fewer tiles.
- *   int8, all layouts   : (64|128|256, 1, 1), (128|256, 2, 1)
+ *   int8, all layouts   : (64|128|256, 1, 1), (128|256, 2, 1), split-K (64|128, 1, 2)
  * The triple must be built for at least one entry point (else
  * DG_ERR_UNSUPPORTED).  An entry point that does not build it keeps the
  * heuristic's choice. */

@@ -631,16 +631,18 @@ using Int8KernelFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, Int8Args);
 // Host-side id of the dense int8 kernels with FP32 output.
 constexpr int MODE_INT8_DENSE_F32 = 3;
 
-template <int BN, int STAGES, int MODE, int CTAS, bool OUT_F32>
+template <int BN, int STAGES, int MODE, int CTAS, bool OUT_F32, int PIPES = 1>
 static Config make_int8_config() {
   Config c;
   c.bn = BN;
   c.stages = STAGES;
   c.ctas = CTAS;
-  c.smem = Int8Layout<BN, STAGES, MODE, CTAS>::kSmemBytes;
+  c.smem = Int8Layout<BN, STAGES, MODE, CTAS, PIPES>::kSmemBytes;
   c.num_acc = 2;
-  c.threads = kInt8Threads;
-  c.fn = reinterpret_cast<KernelFn>(&int8_gemm_kernel<BN, STAGES, MODE, CTAS, OUT_F32>);
+  c.pipes = PIPES;
+  c.splitk = PIPES == 2;
+  c.threads = kInt8Threads<PIPES>;
+  c.fn = reinterpret_cast<KernelFn>(&int8_gemm_kernel<BN, STAGES, MODE, CTAS, OUT_F32, PIPES>);
   return c;
 }
 
@@ -652,7 +654,8 @@ static const Config* int8_config_table(int* count) {
   static const Config table[] = {
       make_int8_config<64, 8, mode, 1, f32>(), make_int8_config<128, 6, mode, 1, f32>(),
       make_int8_config<256, 4, mode, 1, f32>(), make_int8_config<128, 8, mode, 2, f32>(),
-      make_int8_config<256, 6, mode, 2, f32>(),
+      make_int8_config<256, 6, mode, 2, f32>(), make_int8_config<64, 8, mode, 1, f32, 2>(),
+      make_int8_config<128, 6, mode, 1, f32, 2>(),
   };
   *count = static_cast<int>(sizeof(table) / sizeof(table[0]));
   return table;
@@ -663,7 +666,8 @@ static const Config* int8_config_table(int* count) {
 // (512 rows x 4096 x 7168), back to back.
 static const CostParams kCostInt8[] = {
     {64, 1, 1, false, 265, 600},  {128, 1, 1, false, 290, 700},   {256, 1, 1, false, 430, 700},
-    {128, 2, 1, false, 285, 750}, {256, 2, 1, false, 385, 800},
+    {128, 2, 1, false, 285, 750}, {256, 2, 1, false, 385, 800}, {64, 1, 2, true, 385, 900},
+    {128, 1, 2, true, 560, 1000},
 };
 
 // Whether an int8 product is built with this tile (every mode builds the same).
@@ -671,7 +675,7 @@ static bool find_int8_config(int bn, int ctas, int pipes) {
   int n = 0;
   const Config* t = int8_config_table<MODE_DENSE>(&n);
   for (int i = 0; i < n; ++i)
-    if (t[i].bn == bn && (ctas == 0 || t[i].ctas == ctas) && pipes <= 1) return true;
+    if (t[i].bn == bn && (ctas == 0 || t[i].ctas == ctas) && (pipes == 0 || t[i].pipes == pipes)) return true;
   return false;
 }
 
@@ -680,19 +684,20 @@ static const Config* choose_int8_config(long long rows_est, int N, int K, int sm
   constexpr int mode = MODE == MODE_INT8_DENSE_F32 ? MODE_DENSE : MODE;
   int n = 0;
   const Config* t = int8_config_table<MODE>(&n);
-  const auto pairs_fit = [&](const Config& c) {
-    return !(mode == MODE_CONTIG && c.ctas == 2 && rows_est / 128 > kMaxContigBlocks);
+  // pairs within the contiguous layout's table; a K block at least for each of two pipelines
+  const auto fits = [&](const Config& c) {
+    return !(mode == MODE_CONTIG && c.ctas == 2 && rows_est / 128 > kMaxContigBlocks) && !(c.pipes == 2 && K <= 128);
   };
   if (t_force_bn)
     for (int i = 0; i < n; ++i)
-      if (t[i].bn == t_force_bn && (t_force_ctas == 0 || t[i].ctas == t_force_ctas) && t_force_pipes <= 1 &&
-          pairs_fit(t[i]))
+      if (t[i].bn == t_force_bn && (t_force_ctas == 0 || t[i].ctas == t_force_ctas) &&
+          (t_force_pipes == 0 || t[i].pipes == t_force_pipes) && fits(t[i]))
         return &t[i];
   const Config* best = nullptr;
   double best_cost = 1e300;
   for (int i = 0; i < n; ++i) {
     const Config& c = t[i];
-    if (!pairs_fit(c)) continue;
+    if (!fits(c)) continue;
     const CostParams& k = kCostInt8[i];
     const long long tile_m = 128LL * c.ctas;
     long long m_tiles;
@@ -707,7 +712,7 @@ static const Config* choose_int8_config(long long rows_est, int N, int K, int sm
     const long long n_tiles = (N + c.bn - 1) / c.bn;
     const long long units = std::max(1, sms / c.ctas);
     const double waves = static_cast<double>((m_tiles * n_tiles + units - 1) / units);
-    const double compute = waves * (((K + 127) / 128) * k.kb_ns + k.tile_ns);
+    const double compute = waves * (((K + 127) / 128) * (c.splitk ? 0.5 : 1.0) * k.kb_ns + k.tile_ns);
     const double bytes = static_cast<double>(rows_est) * (K + 2.0 * N) +
                          (mode == MODE_DENSE ? 1.0 : groups) * static_cast<double>(N) * K;
     const double memory = bytes / kHbmBytesPerNs;

@@ -12,13 +12,20 @@
 // memory: two accumulators of 256 columns fill it, and the issuing thread has
 // nothing to do but four MMAs and a commit for every 128 of K.  Roles (one
 // CTA per SM, persistent over output tiles):
-//   warp 0     TMEM owner; one thread issues the MMAs (of the pair's first CTA)
-//   warp 1     producer: TMA loads of A/B K-blocks into a STAGES-deep ring
-//   warps 2-9  epilogue: tcgen05.ld, scaling, swizzled staging + TMA store of
+//   issuer     (warp 0, the TMEM owner) one thread issues the MMAs (of the
+//              pair's first CTA)
+//   producer   (warp 1) TMA loads of A/B K-blocks into a STAGES-deep ring
+//   epilogue   (eight warps) tcgen05.ld, scaling, swizzled staging + TMA store of
 //              fully valid 32-row slices, predicated stores for the others
 // CTAS = 2: a cluster of two CTAs computes a 256 x BN tile (cta_group::2), each
 // loading its own 128 rows of A and half of B's.  No load is multicast.
 // A K that is no multiple of 128 ends in a block that the TMA fills with zeros.
+//
+// PIPES = 2 (few rows): a narrow tile's K loop is bound by its issuing thread
+// (some 60 cycles an instruction, 380 a K block against 128 of the tensor core
+// on 64 columns), so two issuers (warps 0, 1) and two producers (warps 2, 3)
+// take half of K each, with half of the ring and an accumulator of their own,
+// which the epilogue adds: integers, so the sum is the same.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -29,16 +36,18 @@
 
 namespace dg {
 
-constexpr int kInt8Threads = 32 * 10;
-constexpr int kInt8Epi0 = 2;  // first epilogue warp
+// An issuer and a producer for each pipeline, and eight epilogue warps.
+template <int PIPES>
+constexpr int kInt8Threads = 32 * (8 + 2 * PIPES);
 
 struct Int8Args : GemmArgs {
   const float* sa;  // [G][rows] (masked) or [rows]
   const float* sb;  // [G][N]
 };
 
-template <int BN, int STAGES, int MODE, int CTAS>
+template <int BN, int STAGES, int MODE, int CTAS, int PIPES>
 struct Int8Layout {
+  static_assert(PIPES == 1 || (PIPES == 2 && CTAS == 1 && STAGES % 2 == 0), "two pipelines run on one CTA");
   static constexpr int kTileM = 128 * CTAS;
   static constexpr int kBRows = BN / CTAS;
   static constexpr int kABytes = 128 * kBK;
@@ -51,7 +60,7 @@ struct Int8Layout {
   static constexpr int kMine = BN / 64;  // 32-column chunks of an epilogue warp
   static constexpr int kOffScale = kOffEpi + 8 * kEpiBuf;  // B's scales of each epilogue warp's chunks
   static constexpr int kOffBar = kOffScale + 8 * kMine * 32 * 4;
-  static constexpr int kNumBars = 2 * STAGES + 2 * 2 + 1;
+  static constexpr int kNumBars = 2 * STAGES + 2 * 2 + PIPES;
   static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kOffGroups = kOffMisc + 16;
   static constexpr int kGroupsBytes = MODE == MODE_MASKED                   ? (2 * kMaxMaskedGroups + 1) * 4
@@ -132,12 +141,14 @@ __device__ __forceinline__ void contig_pair_table(const GemmArgs& p, int* prefix
   if (lane == 0) prefix[0] = count;
 }
 
-template <int BN, int STAGES, int MODE, int CTAS, bool OUT_F32>
-__global__ void __launch_bounds__(kInt8Threads, 1)
+template <int BN, int STAGES, int MODE, int CTAS, bool OUT_F32, int PIPES>
+__global__ void __launch_bounds__(kInt8Threads<PIPES>, 1)
     int8_gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                      const __grid_constant__ CUtensorMap tm_d, const Int8Args p) {
-  using L = Int8Layout<BN, STAGES, MODE, CTAS>;
+  using L = Int8Layout<BN, STAGES, MODE, CTAS, PIPES>;
   constexpr bool kPair = CTAS == 2;
+  constexpr int kRing = STAGES / PIPES;  // stages of a pipeline
+  constexpr int kEpi0 = 2 * PIPES;       // first epilogue warp
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -157,7 +168,14 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
-  const int num_kb = (p.K + kBK - 1) / kBK;
+  const bool is_issuer = warp < PIPES, is_producer = warp >= PIPES && warp < kEpi0;
+  const int pipe = PIPES == 2 ? warp & 1 : 0;  // of an issuer or a producer
+  // the pipeline's K blocks and stages
+  const int all_kb = (p.K + kBK - 1) / kBK;
+  const int half_kb = (all_kb + 1) / 2;
+  const int kb_lo = PIPES == 2 && pipe == 1 ? half_kb : 0;
+  const int kb_hi = PIPES == 2 && pipe == 0 ? half_kb : all_kb;
+  const int s_lo = pipe * kRing;
   const uint32_t rank = kPair ? cluster_cta_rank() : 0;
   const int unit0 = kPair ? static_cast<int>(blockIdx.x / 2) : static_cast<int>(blockIdx.x);
   const int units = kPair ? static_cast<int>(gridDim.x / 2) : static_cast<int>(gridDim.x);
@@ -172,7 +190,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
       mbar_init(&tmem_full[i], 1);
       mbar_init(&tmem_empty[i], 8 * CTAS);
     }
-    mbar_init(final_bar, 1);
+    for (int i = 0; i < PIPES; ++i) mbar_init(&final_bar[i], 1);
     *abort_flag = 0;
     *all_landed = 0;
     fence_barrier_init();
@@ -187,15 +205,15 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
   }
   grid_dep_wait();
   grid_dep_launch();
-  if (MODE == MODE_MASKED && warp == kInt8Epi0) masked_tile_prefix<L::kTileM>(p, prefix, counts, lane);
-  if (MODE == MODE_CONTIG && kPair && warp == kInt8Epi0) contig_pair_table(p, prefix, lane);
+  if (MODE == MODE_MASKED && warp == kEpi0) masked_tile_prefix<L::kTileM>(p, prefix, counts, lane);
+  if (MODE == MODE_CONTIG && kPair && warp == kEpi0) contig_pair_table(p, prefix, lane);
   tc_fence_before();
   if constexpr (kPair) cluster_sync(); else __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   const int ntiles = total_tiles<MODE, CTAS>(p, prefix);
 
-  if (warp == 1) {
+  if (is_producer) {
     // ============================================================ producer
     const uint32_t full0 = kPair ? mapa_shared(smem_u32(full_bar), 0) : smem_u32(full_bar);
     bool ok = true;
@@ -212,9 +230,9 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
       const int n0 = tl.n_blk * BN;
       // each CTA of a pair holds half of the tile's MMA width of B
       const int b_row = n0 + static_cast<int>(rank) * (tile_mma_n<BN, CTAS, 0>(n0, p.N) / CTAS);
-      for (int kb = 0; kb < num_kb; ++kb, ++it) {
-        const uint32_t s = it % STAGES;
-        ok = wait_phase<false>(&empty_bar[s], ((it / STAGES) & 1) ^ 1, abort_flag, p.wait_limit_ns);
+      for (int kb = kb_lo; kb < kb_hi; ++kb, ++it) {
+        const uint32_t s = s_lo + it % kRing;
+        ok = wait_phase<false>(&empty_bar[s], ((it / kRing) & 1) ^ 1, abort_flag, p.wait_limit_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
@@ -232,25 +250,25 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         }
       }
     }
-    // Every load must land before its CTA exits: alone, the last STAGES loads
-    // are waited for here; in a pair all loads signal the first CTA, which
+    // Every load must land before its CTA exits: alone, the last loads of the
+    // ring are waited for here; in a pair all loads signal the first CTA, which
     // drains both after the cluster barrier of the teardown.
     if constexpr (!kPair) {
       if (lane == 0) {
-        for (uint32_t i = it > STAGES ? it - STAGES : 0; i < it; ++i)
-          wait_phase_drain(&full_bar[i % STAGES], (i / STAGES) & 1);
+        for (uint32_t i = it > kRing ? it - kRing : 0; i < it; ++i)
+          wait_phase_drain(&full_bar[s_lo + i % kRing], (i / kRing) & 1);
       }
     } else if (rank == 1 && lane == 0) {
       st_shared_cluster_u32(mapa_shared(smem_u32(peer_loads), 0), it);
       fence_cluster();
     }
     __syncwarp();
-  } else if (warp == 0) {
+  } else if (is_issuer) {
     // ============================================================ MMA issuer
     if ((!kPair || rank == 0) && lane == 0) {
-      const uint64_t a0 = make_smem_desc(smem_u32(smem), 16, 1024, 2);
-      const uint64_t b0 = make_smem_desc(smem_u32(smem + L::kOffB), 16, 1024, 2);
-      const uint32_t full_base = smem_u32(full_bar), empty_base = smem_u32(empty_bar);
+      const uint64_t a0 = make_smem_desc(smem_u32(smem + s_lo * L::kABytes), 16, 1024, 2);
+      const uint64_t b0 = make_smem_desc(smem_u32(smem + L::kOffB + s_lo * L::kBBytes), 16, 1024, 2);
+      const uint32_t full_base = smem_u32(full_bar + s_lo), empty_base = smem_u32(empty_bar + s_lo);
       uint32_t s = 0, phase = 0, own = 0;
       bool ok = true;
       const bool ragged_n = p.N % BN != 0;
@@ -262,7 +280,8 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
           mma_n = tile_mma_n<BN, CTAS, 0>(tl.n_blk * BN, p.N);
         }
         const uint32_t idesc = make_idesc_i8(L::kTileM, mma_n);
-        const uint32_t acc = own & 1, use = own >> 1;
+        // one pipeline alternates the accumulators, two have one each
+        const uint32_t acc = PIPES == 2 ? pipe : own & 1, use = PIPES == 2 ? own : own >> 1;
         ++own;
         if (!mbar_try_wait(&tmem_empty[acc], (use & 1) ^ 1))
           ok = wait_phase<false>(&tmem_empty[acc], (use & 1) ^ 1, abort_flag, p.wait_limit_ns);
@@ -275,16 +294,16 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         // the MMAs of this one.
         uint32_t accumulate = 0;
         bool ready = mbar_test_wait_addr(full_base + 8 * s, phase);
-        for (int kb = 0; kb < num_kb; ++kb) {
+        for (int kb = kb_lo; kb < kb_hi; ++kb) {
           if (!ready && !mbar_try_wait_addr(full_base + 8 * s, phase)) {
-            ok = wait_phase<false>(&full_bar[s], phase, abort_flag, p.wait_limit_ns);
+            ok = wait_phase<false>(&full_bar[s_lo + s], phase, abort_flag, p.wait_limit_ns);
             if (!ok) break;
           }
           const uint64_t a = a0 + s * (L::kABytes >> 4), b = b0 + s * (L::kBBytes >> 4);
           const uint32_t done = empty_base + 8 * s;
           mma_i8<CTAS>(d_tmem, a, b, idesc, accumulate);
           mma_i8<CTAS>(d_tmem, a + 2, b + 2, idesc, 1u);
-          if (++s == STAGES) {
+          if (++s == kRing) {
             s = 0;
             phase ^= 1;
           }
@@ -300,8 +319,8 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         else tc_commit<1>(&tmem_full[acc]);
       }
       // all MMAs issued here complete before TMEM is freed
-      tc_commit<CTAS>(final_bar);
-      wait_phase_drain(final_bar, 0);
+      tc_commit<CTAS>(&final_bar[pipe]);
+      wait_phase_drain(&final_bar[pipe], 0);
       if constexpr (kPair) {
         if (ok) {
           const uint32_t at = smem_u32(const_cast<uint32_t*>(all_landed));
@@ -318,7 +337,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     // 32-column chunks; the next chunk's tcgen05.ld is in flight while the
     // current one is scaled and stored.
     const int q = warp % 4;
-    const int epi = warp - kInt8Epi0;
+    const int epi = warp - kEpi0;
     const int half = epi >> 2;
     uint8_t* buf = smem + L::kOffEpi + epi * L::kEpiBuf;
     const uint32_t empty0 = kPair ? mapa_shared(smem_u32(tmem_empty), 0) : smem_u32(tmem_empty);
@@ -331,13 +350,13 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
       if (MODE == MODE_CONTIG) {
         const int own_blk = tl.row0 / 128 + static_cast<int>(rank);  // a pair's blocks may differ in expert
         own_e = own_blk < p.rows / 128 ? __ldg(&p.m_indices[own_blk * 128]) : -1;
-        if ((own_e < -1 || own_e >= p.G) && warp == kInt8Epi0 && lane == 0 && tl.n_blk == 0) atomicOr(&g_dg_error, 0x2);
+        if ((own_e < -1 || own_e >= p.G) && warp == kEpi0 && lane == 0 && tl.n_blk == 0) atomicOr(&g_dg_error, 0x2);
         expert = contig_expert<CTAS>(tl, p);
         if (expert < 0) continue;
       } else if (MODE == MODE_MASKED) {
         expert = tl.g;
       }
-      const uint32_t acc = own & 1, use = own >> 1;
+      const uint32_t acc = PIPES == 2 ? 0 : own & 1, use = PIPES == 2 ? own : own >> 1;
       ++own;
       const int row0 = tl.row0 + 128 * static_cast<int>(rank) + 32 * q;  // the warp's first row
       const int m = row0 + lane;
@@ -369,6 +388,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
       const uint32_t t_row = tmem_base + (static_cast<uint32_t>(32 * q) << 16) + acc * L::kAccStride;
 
       bool ok = wait_phase<false>(&tmem_full[acc], use & 1, abort_flag, p.wait_limit_ns);
+      if (PIPES == 2 && ok) ok = wait_phase<false>(&tmem_full[1], use & 1, abort_flag, p.wait_limit_ns);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -436,6 +456,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         if (lane == 0) {
           if constexpr (kPair) mbar_arrive_remote(empty0 + 8 * acc);
           else mbar_arrive(&tmem_empty[acc]);
+          if (PIPES == 2) mbar_arrive(&tmem_empty[1]);
         }
       };
       const int mine = any_valid ? min(kMine, max(0, ((p.N - n0 + 31) / 32 - half + 1) / 2)) : 0;
@@ -451,7 +472,17 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
         if (i >= mine) break;
         const int c = half + 2 * i;
         if (i + 1 < mine) tmem_ld_32x32b_x32(t_row + 32 * (c + 2), r[(i + 1) & 1]);
-        else release();
+        if constexpr (PIPES == 2) {  // the other half of K
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(t_row + L::kAccStride + 32 * c + 16 * h, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) r[i & 1][16 * h + j] += o[j];
+          }
+        }
+        if (i + 1 == mine) release();
         finish(r[i & 1], n0 + 32 * c, sbuf + 32 * i);
         if (i + 1 < mine) tmem_wait_ld();
       }
@@ -468,7 +499,7 @@ __global__ void __launch_bounds__(kInt8Threads, 1)
     // visible; the epilogue's global stores need not be waited for.
     cluster_sync_relaxed();
     if (!*all_landed) {
-      if (rank == 0 && warp == 1 && lane == 0) {
+      if (rank == 0 && is_producer && lane == 0) {
         // A CTA that gave up before issuing load j never arrives: arrive in its
         // place, then wait for the loads that were issued.
         const uint32_t it1 = *reinterpret_cast<volatile uint32_t*>(peer_loads);

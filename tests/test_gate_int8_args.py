@@ -127,15 +127,19 @@ def test_int8_tile_choice(lib):
     """The heuristic is host logic (148 SMs assumed without a device): narrow
     1-CTA tiles for a few rows, pairs of CTAs for many, no pairs beyond the
     contiguous layout's table; a forced tile holds where it is built."""
-    assert dg.describe_config("int8_dense", 64, 7168, 2048) == "128x64x8/112"
+    assert dg.describe_config("int8_dense", 64, 7168, 2048) == "128x64x8(2pipe)(splitk)/112"
+    assert "(splitk)" not in dg.describe_config("int8_dense", 64, 7168, 128)      # one K block
     assert dg.describe_config("int8_dense", 4096, 7168, 2048).startswith("256x256x6(2cta)")
+    assert dg.describe_config("int8_contiguous", 4096, 4096, 7168, 8).startswith("256x256x6(2cta)")
     assert dg.describe_config("int8_contiguous", 32768, 4096, 7168, 8) == "256x256x6(2cta)/148"
     assert "(2cta)" not in dg.describe_config("int8_contiguous", 1024 * 128 + 128, 4096, 7168, 8)
     assert dg.describe_config("int8_masked", 256, 7168, 2048, 16).startswith("128x256")
     assert lib.dg_set_config(128, 2, 1) == 0
     try:
         assert dg.describe_config("int8_dense", 64, 7168, 2048).startswith("256x128x8(2cta)")
+        assert lib.dg_set_config(64, 1, 2) == 0
+        assert "(splitk)" not in dg.describe_config("int8_dense", 64, 7168, 128)
         assert lib.dg_set_config(224, 2, 2) == 0          # not built for int8: the choice stands
-        assert dg.describe_config("int8_dense", 64, 7168, 2048) == "128x64x8/112"
+        assert dg.describe_config("int8_dense", 64, 7168, 2048) == "128x64x8(2pipe)(splitk)/112"
     finally:
         assert lib.dg_set_config(0, 0, 0) == 0

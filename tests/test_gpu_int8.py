@@ -18,7 +18,7 @@ from oracle import routing
 from helpers import bits, check_close
 
 pytestmark = pytest.mark.gpu
-CONFIGS = [(64, 1, 1), (128, 1, 1), (256, 1, 1), (128, 2, 1), (256, 2, 1)]
+CONFIGS = [(64, 1, 1), (128, 1, 1), (256, 1, 1), (128, 2, 1), (256, 2, 1), (64, 1, 2), (128, 1, 2)]
 
 
 @pytest.fixture(autouse=True)
@@ -218,12 +218,13 @@ def test_no_rows_is_nothing():
     assert q.shape == (0, 64) and s.shape == (0,)
 
 
-def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+@pytest.mark.parametrize("cfg", [(128, 1, 1), (64, 1, 2)])
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(cfg):
     rng = np.random.default_rng(9)
     M, N, K = 128, 512, 32768
     (a, sa), (b, sb) = _codes(rng, M, K), _codes(rng, N, K)
     t = _cuda(a, sa, b, sb)
-    dg.set_config(128, 1, 1)
+    dg.set_config(*cfg)
     prev = dg.set_wait_limit_ns(0)
     try:
         dg.int8_gemm_nt(*t)
