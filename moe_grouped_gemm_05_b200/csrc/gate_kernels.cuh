@@ -401,6 +401,11 @@ __device__ __noinline__ int gate_choose64(const GateArgs& p, const LT* row, int 
 // closer below it than `near`) are put together in shared memory, and each
 // lane counts the ones before its own.  That takes the place of topk rounds of
 // finding and removing the best (which serve the rows with more than 32).
+//
+// Measured, 16384 tokens: 256 experts in 8 groups, topk 8, 15.9 us (topk rounds
+// 37.9); without groups 13.2, without bias 11.3; 64 experts, softmax, topk 6,
+// 5.9 us (a whole warp a token 9.4).  Bound by issue: 709 instructions a token of
+// 256 experts; more resident warps or larger blocks change nothing.
 template <typename LT, int L, int V, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_constant__ GateArgs p) {
   constexpr int kTeams = 32 * kGateWarps / L;
@@ -751,7 +756,9 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
 // ---------------------------------------------------------------- backward
 
 // One warp a token: lane j holds slot j, the row is put together in shared
-// memory and written once.
+// memory and written once.  16384 x 256 FP32, topk 8: 6.8 us (2.7 TB/s, the rows
+// coming from L2), dense softmax 7.7 us; bound by the latency of the gathered
+// logits and of the sums, which one row's warp cannot overlap.
 template <typename LT, int V>
 __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(const GateBackwardArgs p) {
   __shared__ __align__(16) float rows[kGateWarps][32 * V];

@@ -21,11 +21,18 @@
 // loading its own 128 rows of A and half of B's.  No load is multicast.
 // A K that is no multiple of 128 ends in a block that the TMA fills with zeros.
 //
+// Measured (BF16 out): 4096x7168x2048 45.4 us, 2.65 POPS; 82% of the busiest
+// SM's cycles are MMAs, the rest set-up, first load, last epilogue and teardown.
+// Contiguous, 8 experts, 32768 rows, 4096x7168: 600 us before the power cap sets
+// in (3.2 POPS), 735 us under it.  Masked, 16 experts of up to 256 rows,
+// 7168x2048: 53 us, 5 rounds of 128x256 tiles.
+//
 // PIPES = 2 (few rows): a narrow tile's K loop is bound by its issuing thread
 // (some 60 cycles an instruction, 380 a K block against 128 of the tensor core
 // on 64 columns), so two issuers (warps 0, 1) and two producers (warps 2, 3)
 // take half of K each, with half of the ring and an accumulator of their own,
-// which the epilogue adds: integers, so the sum is the same.
+// which the epilogue adds: integers, so the sum is the same.  64x7168x2048: 5.5 us
+// against 7.5 with one pipeline; 64x4096x7168 12.5 against 18.6.
 #pragma once
 #include <cuda_bf16.h>
 #include <cstdint>

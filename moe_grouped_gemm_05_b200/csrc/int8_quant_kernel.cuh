@@ -197,8 +197,9 @@ __global__ void __launch_bounds__(U == 4 && sizeof(T) == 4 ? 512 : 1024) quantiz
 }
 
 // Routing, quantisation and scattering of few slots (a decode batch) in one
-// launch.  The routing kernel's cluster takes about 8 us whatever the batch
-// (its counting passes, two cluster barriers, a table of 32 counts an expert);
+// launch: 64 tokens, top-8 of 256, K = 2048 3.4 us against 10.4.  The routing
+// kernel's cluster takes 7 to 10 us whatever the batch (its counting passes, two
+// cluster barriers, a table of 32 counts an expert);
 // here every block counts the experts of all slots and scans the segments for
 // itself, and ranks only its own token's slots among the earlier ones.  Blocks
 // behind the last token only mark padding rows.
