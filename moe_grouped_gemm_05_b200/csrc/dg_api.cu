@@ -841,13 +841,26 @@ static cudaError_t launch_quantize_permute_few(const QuantArgs& p, int sms, cuda
   return launch_plain(quantize_permute_few_kernel<T, 0>, blocks, kFewThreads, st, p);
 }
 
-// The gate kernel for teams of L lanes with V experts each.
+// Lanes of a team of L that each of n_group groups can have, and the experts of
+// a lane then (without groups: of the row's runs).
+static void gate_split(const GateArgs& p, int L, int* span, int* width) {
+  int groups = 1;
+  while (groups < p.n_group) groups *= 2;
+  *span = L / groups;
+  *width = (p.gsize + *span - 1) / *span;
+}
+
+// The gate kernel for teams of L lanes with up to V experts each.
 template <typename T, int L, int V>
 static cudaError_t launch_gate_v(GateArgs& p, cudaStream_t st) {
-  const int span = p.gsize / V;
+  int span = 0;
+  gate_split(p, L, &span, &p.width);
   p.span_log2 = -1;
-  if (p.gsize % V == 0 && (span & (span - 1)) == 0)
+  if (p.n_group > 1 && p.width <= V)
     for (p.span_log2 = 0; (1 << p.span_log2) < span;) ++p.span_log2;
+  p.vec = p.span_log2 >= 0 ? p.width == V && p.gsize % V == 0 : p.E % V == 0;
+  p.full = p.vec && p.E == L * V;
+  p.deal = p.span_log2 >= 0 && p.topk_group * span < 2 * p.topk;
   constexpr int th = 32 * kGateWarps, per = th / L;
   const long long blocks = (static_cast<long long>(p.T) + per - 1) / per;
   if (p.sigmoid)
@@ -856,26 +869,27 @@ static cudaError_t launch_gate_v(GateArgs& p, cudaStream_t st) {
   return p.bias ? launch_plain(moe_gate_kernel<T, L, V, false, true>, blocks, th, st, p)
                 : launch_plain(moe_gate_kernel<T, L, V, false, false>, blocks, th, st, p);
 }
-// Half a warp a token for up to 128 experts, where its 16 lanes can hold the
-// slots and groups and the kernel's list stays short: no more than 32 experts
-// in the kept groups, or twice as many lanes with such experts as slots.
-// Measured at 16384 tokens: 64 experts, topk 6 6.4 us (a whole warp: 9.4), 128
-// experts, topk 8 with a bias 11.4 us (12.5); with 128 experts in 4 groups, 2
-// kept, 22 us against 15: there the whole warp.
+// Half a warp a token for up to 128 experts, where its 16 lanes hold the slots and
+// groups and the kernel's list stays short: at most half as many slots as lanes, or
+// no more than 32 experts in the kept groups.  Measured at 16384 tokens: 64 experts,
+// topk 6 6.2 us (a whole warp: 9.4), 128 experts, topk 8 with a bias 9.4 us (12.5).
 template <typename T>
 static cudaError_t launch_gate(GateArgs& p, cudaStream_t st) {
+  if (p.n_group == 1) p.gsize = p.E;
+  int span = 0, width = 0;
   const int left = p.n_group > 1 ? p.topk_group * p.gsize : p.E;  // experts in the kept groups
-  const int v = p.E <= 32 ? 2 : p.E <= 64 ? 4 : 8;
-  if (p.E <= 128 && p.topk <= 16 && p.n_group <= 16 && (left <= kGateList || left / v >= 2 * p.topk)) {
-    if (v == 2) return launch_gate_v<T, 16, 2>(p, st);
-    if (v == 4) return launch_gate_v<T, 16, 4>(p, st);
-    return launch_gate_v<T, 16, 8>(p, st);
+  if (p.E <= 128 && p.topk <= 16 && p.n_group <= 16 && (p.topk <= 8 || left <= kGateList)) {
+    gate_split(p, 16, &span, &width);
+    if (width <= 2) return launch_gate_v<T, 16, 2>(p, st);
+    if (width <= 4) return launch_gate_v<T, 16, 4>(p, st);
+    if (width <= 8) return launch_gate_v<T, 16, 8>(p, st);
   }
-  if (p.E <= 32) return launch_gate_v<T, 32, 1>(p, st);
-  if (p.E <= 64) return launch_gate_v<T, 32, 2>(p, st);
-  if (p.E <= 128) return launch_gate_v<T, 32, 4>(p, st);
-  if (p.E <= 256) return launch_gate_v<T, 32, 8>(p, st);
-  if (p.E <= 512) return launch_gate_v<T, 32, 16>(p, st);
+  gate_split(p, 32, &span, &width);
+  if (width <= 1) return launch_gate_v<T, 32, 1>(p, st);
+  if (width <= 2) return launch_gate_v<T, 32, 2>(p, st);
+  if (width <= 4) return launch_gate_v<T, 32, 4>(p, st);
+  if (width <= 8) return launch_gate_v<T, 32, 8>(p, st);
+  if (width <= 16) return launch_gate_v<T, 32, 16>(p, st);
   return launch_gate_v<T, 32, 32>(p, st);
 }
 template <typename T>

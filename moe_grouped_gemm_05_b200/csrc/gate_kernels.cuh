@@ -41,7 +41,10 @@ struct GateArgs {
   int T, E, topk;
   int n_group, topk_group, group_top;
   int gsize;            // experts of a group
-  int span_log2;        // a group is 2^span_log2 whole lanes, or -1
+  int span_log2;        // a group belongs to 2^span_log2 lanes of its own, `width` experts each; or -1
+  int width;
+  int vec, full;        // every lane holds one aligned run of V experts or none; every lane holds V
+  int deal;             // the kept groups' experts are dealt out over all lanes
   int sigmoid, renorm;
   float scale;
   int32_t* ids;         // [T][topk]
@@ -59,21 +62,21 @@ struct GateBackwardArgs {
 };
 
 // ---------------------------------------------------------------- rows in registers
-// Lane t of the warp holds elements [t*V, t*V + V) of a row; those behind its
-// end read as `fill`.  With E % V == 0 a lane's elements are one aligned run,
-// moved in accesses of up to 16 bytes.
+// A lane holds `live` <= V elements of a row, from `first` on and `step` apart; the
+// others read as `fill`.  vec: every lane has V of them or none, in aligned runs,
+// which are moved in accesses of up to 16 bytes.
 
 template <int V>
-__device__ __forceinline__ void gate_load_row(const float* row, int E, int lane, float fill, float (&l)[V]) {
-  const int e0 = lane * V;
-  if (E % V == 0) {
-    if (e0 >= E) {
+__device__ __forceinline__ void gate_load_row(const float* row, int first, int step, int live, bool vec,
+                                              float fill, float (&l)[V]) {
+  if (vec) {
+    if (live == 0) {
 #pragma unroll
       for (int i = 0; i < V; ++i) l[i] = fill;
     } else if constexpr (V >= 4) {
 #pragma unroll
       for (int i = 0; i < V / 4; ++i) {
-        const float4 v = __ldg(reinterpret_cast<const float4*>(row + e0) + i);
+        const float4 v = __ldg(reinterpret_cast<const float4*>(row + first) + i);
         l[4 * i] = v.x;
         l[4 * i + 1] = v.y;
         l[4 * i + 2] = v.z;
@@ -81,25 +84,25 @@ __device__ __forceinline__ void gate_load_row(const float* row, int E, int lane,
       }
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) l[i] = __ldg(row + e0 + i);
+      for (int i = 0; i < V; ++i) l[i] = __ldg(row + first + i);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = e0 + i < E ? __ldg(row + e0 + i) : fill;
+    for (int i = 0; i < V; ++i) l[i] = i < live ? __ldg(row + first + i * step) : fill;
   }
 }
 
 template <int V>
-__device__ __forceinline__ void gate_load_row(const __nv_bfloat16* row, int E, int lane, float fill, float (&l)[V]) {
-  const int e0 = lane * V;
-  if (E % V == 0) {
-    if (e0 >= E) {
+__device__ __forceinline__ void gate_load_row(const __nv_bfloat16* row, int first, int step, int live, bool vec,
+                                              float fill, float (&l)[V]) {
+  if (vec) {
+    if (live == 0) {
 #pragma unroll
       for (int i = 0; i < V; ++i) l[i] = fill;
     } else if constexpr (V >= 8) {
 #pragma unroll
       for (int i = 0; i < V / 8; ++i) {
-        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + e0) + i);
+        const uint4 v = __ldg(reinterpret_cast<const uint4*>(row + first) + i);
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -110,36 +113,36 @@ __device__ __forceinline__ void gate_load_row(const __nv_bfloat16* row, int E, i
     } else if constexpr (V >= 2) {
 #pragma unroll
       for (int i = 0; i < V / 2; ++i) {
-        const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(row + e0) + i);
+        const uint32_t u = __ldg(reinterpret_cast<const uint32_t*>(row + first) + i);
         l[2 * i] = __uint_as_float(u << 16);
         l[2 * i + 1] = __uint_as_float(u & 0xFFFF0000u);
       }
     } else {
-      l[0] = __bfloat162float(row[e0]);
+      l[0] = __bfloat162float(row[first]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = e0 + i < E ? __bfloat162float(row[e0 + i]) : fill;
+    for (int i = 0; i < V; ++i) l[i] = i < live ? __bfloat162float(row[first + i * step]) : fill;
   }
 }
 
 template <int V>
-__device__ __forceinline__ void gate_store_row(float* row, int E, int lane, const float (&l)[V]) {
-  const int e0 = lane * V;
-  if (E % V == 0) {
-    if (e0 >= E) return;
+__device__ __forceinline__ void gate_store_row(float* row, int first, int step, int live, bool vec,
+                                               const float (&l)[V]) {
+  if (vec) {
+    if (live == 0) return;
     if constexpr (V >= 4) {
 #pragma unroll
       for (int i = 0; i < V / 4; ++i)
-        reinterpret_cast<float4*>(row + e0)[i] = make_float4(l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
+        reinterpret_cast<float4*>(row + first)[i] = make_float4(l[4 * i], l[4 * i + 1], l[4 * i + 2], l[4 * i + 3]);
     } else {
 #pragma unroll
-      for (int i = 0; i < V; ++i) row[e0 + i] = l[i];
+      for (int i = 0; i < V; ++i) row[first + i] = l[i];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (e0 + i < E) row[e0 + i] = l[i];
+      if (i < live) row[first + i * step] = l[i];
   }
 }
 
@@ -149,26 +152,26 @@ __device__ __forceinline__ uint32_t gate_bf16x2(float lo, float hi) {
 }
 
 template <int V>
-__device__ __forceinline__ void gate_store_row(__nv_bfloat16* row, int E, int lane, const float (&l)[V]) {
-  const int e0 = lane * V;
-  if (E % V == 0) {
-    if (e0 >= E) return;
+__device__ __forceinline__ void gate_store_row(__nv_bfloat16* row, int first, int step, int live, bool vec,
+                                               const float (&l)[V]) {
+  if (vec) {
+    if (live == 0) return;
     if constexpr (V >= 8) {
 #pragma unroll
       for (int i = 0; i < V / 8; ++i)
-        reinterpret_cast<uint4*>(row + e0)[i] =
+        reinterpret_cast<uint4*>(row + first)[i] =
             make_uint4(gate_bf16x2(l[8 * i], l[8 * i + 1]), gate_bf16x2(l[8 * i + 2], l[8 * i + 3]),
                        gate_bf16x2(l[8 * i + 4], l[8 * i + 5]), gate_bf16x2(l[8 * i + 6], l[8 * i + 7]));
     } else if constexpr (V >= 2) {
 #pragma unroll
-      for (int i = 0; i < V / 2; ++i) reinterpret_cast<uint32_t*>(row + e0)[i] = gate_bf16x2(l[2 * i], l[2 * i + 1]);
+      for (int i = 0; i < V / 2; ++i) reinterpret_cast<uint32_t*>(row + first)[i] = gate_bf16x2(l[2 * i], l[2 * i + 1]);
     } else {
-      row[e0] = __float2bfloat16_rn(l[0]);
+      row[first] = __float2bfloat16_rn(l[0]);
     }
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i)
-      if (e0 + i < E) row[e0 + i] = __float2bfloat16_rn(l[i]);
+      if (i < live) row[first + i * step] = __float2bfloat16_rn(l[i]);
   }
 }
 
@@ -402,10 +405,12 @@ __device__ __noinline__ int gate_choose64(const GateArgs& p, const LT* row, int 
 // lane counts the ones before its own.  That takes the place of topk rounds of
 // finding and removing the best (which serve the rows with more than 32).
 //
-// Measured, 16384 tokens: 256 experts in 8 groups, topk 8, 15.9 us (topk rounds
-// 37.9); without groups 13.2, without bias 11.3; 64 experts, softmax, topk 6,
-// 5.9 us (a whole warp a token 9.4).  Bound by issue: 709 instructions a token of
-// 256 experts; more resident warps or larger blocks change nothing.
+// Measured, 16384 tokens: 256 experts in 8 groups, topk 8, 16.3 us (topk rounds
+// 37.9); without groups 13.4, without bias 11.6; 64 experts, softmax, topk 6,
+// 6.2 us (a whole warp a token 9.4); 160 experts in 8 groups, 3 kept, 18.8 us (47.6
+// before groups of any size had lanes of their own and few kept experts were dealt
+// out).  Bound by issue, some 710 instructions a token of 256 experts; more resident
+// warps or larger blocks change nothing.
 template <typename LT, int L, int V, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_constant__ GateArgs p) {
   constexpr int kTeams = 32 * kGateWarps / L;
@@ -427,11 +432,27 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
 
   const bool sums = p.n_group > 1 && p.group_top > 1;
   const bool scored = BIAS || sums;
-  const bool full = p.E == L * V;  // every lane holds V experts
-  const int live = full ? V : min(V, max(0, p.E - tl * V));
+  // This lane's experts.  With groups, each group has lanes of its own (where its
+  // experts fit into them); without, a row of whole runs of V is cut into those,
+  // and any other is dealt out an expert at a time.  (Whole runs come out as the
+  // first line has them in both ways.)
+  int first = tl * V, step = 1, live = first < p.E ? V : 0;
+  if (!p.vec) {
+    if (p.n_group == 1) {
+      first = tl;
+      step = L;
+      live = max(0, (p.E - tl + L - 1) / L);
+    } else if (p.span_log2 >= 0) {
+      const int g = tl >> p.span_log2, part = (tl & ((1 << p.span_log2) - 1)) * p.width;
+      first = g * p.gsize + part;
+      live = g < p.n_group ? min(p.width, max(0, p.gsize - part)) : 0;
+    } else {
+      live = min(V, max(0, p.E - first));
+    }
+  }
   float l[V], c[V];
-  gate_load_row<V>(row, p.E, tl, -FLT_MAX, l);
-  if (BIAS) gate_load_row<V>(p.bias, p.E, tl, 0.0f, c);
+  gate_load_row<V>(row, first, step, live, p.vec, -FLT_MAX, l);
+  if (BIAS) gate_load_row<V>(p.bias, first, step, live, p.vec, 0.0f, c);
   float big = 0.0f, largest = 0.0f;  // the largest |logit| and |bias|: below infinity when nothing is masked or bad
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -471,7 +492,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       bad |= i < live && !(l[i] < INFINITY);
       if (l[i] == -INFINITY) c[i] = -INFINITY;
       if (BIAS) {
-        const float b = i < live ? __ldg(p.bias + tl * V + i) : 0.0f;
+        const float b = i < live ? __ldg(p.bias + first + i * step) : 0.0f;
         bad |= !(b < INFINITY);
         if (b == -INFINITY) c[i] = -INFINITY;
         largest = fmaxf(i == 0 ? 0.0f : largest, b > -INFINITY ? fabsf(b) : 0.0f);
@@ -489,16 +510,19 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
     largest = team_max<L>(largest);
     near += 0x1p-23f * (1.0f + largest);
   }
-  if (!full) {
+  if (!p.full) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (i >= live) c[i] = -INFINITY;
   }
+  int expert[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) expert[i] = first + i * step;
 
   bool unsure = false;  // the token needs the choice in 64 bits (the team agrees)
   if (p.n_group > 1) {
     const bool whole = p.span_log2 >= 0;
-    const int span = whole ? 1 << p.span_log2 : 1;  // lanes that hold the same group
+    const int span = whole ? 1 << p.span_log2 : 1;
     const int at = whole ? tl >> p.span_log2 : tl;  // the group whose score this lane holds
     float mine;
     float a1 = c[0], a2 = -INFINITY;
@@ -549,7 +573,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
         for (int i = 0; i < V; ++i)
           if (c[i] >= lowest && c[i] > -INFINITY) {
             e2 = e1;
-            e1 = tl * V + i;
+            e1 = first + i;
             ++n;
           }
         for (int o = 1; o < span; o <<= 1) {
@@ -583,17 +607,36 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
         }
       }
     }
-    if (whole) {
+    if (!BIAS && sums) {  // the groups went by scores, their experts go by the logits
+#pragma unroll
+      for (int i = 0; i < V; ++i) c[i] = c[i] == -INFINITY ? c[i] : l[i];
+    }
+    if (p.deal) {
+      // Few lanes have experts left: these, in order, are dealt out over all lanes,
+      // so that the best of the lanes tell more about the best of the row.
+      const uint32_t heads = team_ballot<L>(kept && (tl & (span - 1)) == 0, lane);
+      const int to = __popc(heads & ((1u << (at << p.span_log2)) - 1u)) * p.gsize + (first - at * p.gsize);
+      if (kept) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (i < live) list[to + i] = make_float2(c[i], __int_as_float(first + i));
+      }
+      const int left = __popc(heads) * p.gsize;
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float2 x = tl + L * i < left ? list[tl + L * i] : make_float2(-INFINITY, 0.0f);
+        c[i] = x.x;
+        expert[i] = __float_as_int(x.y);
+      }
+      __syncwarp();
+    } else if (whole) {
 #pragma unroll
       for (int i = 0; i < V; ++i) c[i] = kept ? c[i] : -INFINITY;
     } else {
 #pragma unroll
       for (int i = 0; i < V; ++i)
         if (!__shfl_sync(0xffffffffu, kept, min(L - 1, (tl * V + i) / p.gsize), L)) c[i] = -INFINITY;
-    }
-    if (!BIAS && sums) {  // the groups went by scores, their experts go by the logits
-#pragma unroll
-      for (int i = 0; i < V; ++i) c[i] = c[i] == -INFINITY ? c[i] : l[i];
     }
   }
 
@@ -611,7 +654,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
   __syncwarp();
   uint32_t to = smem_u32(list) + 8 * (n > 0 ? atomicAdd(count, n) : 0);
 #pragma unroll
-  for (int i = 0; i < V; ++i) list_from(to, c[i], tl * V + i, bound);
+  for (int i = 0; i < V; ++i) list_from(to, c[i], expert[i], bound);
   __syncwarp();
   const int all = *count;
   const int m = min(all, kGateList);
@@ -698,27 +741,28 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
 #pragma unroll
       for (int i = 1; i < V; ++i) lead = fmaxf(lead, c[i]);
       const float next = team_max<L>(lead);
-      const uint32_t who = __ballot_sync(0xffffffffu, lead == next && next > -INFINITY) >> (lane & ~(L - 1));
-      const int src = __ffs(L == 32 ? who : who & ((1u << (L & 31)) - 1u)) - 1;  // -1: none is left
-      int e = -1;
-      if (tl == src) {
-        bool found = false;
+      // of equal ones the expert with the lowest index (a lane's experts are in order)
+      int e = 0x7FFFFFFF;
+#pragma unroll
+      for (int i = V - 1; i >= 0; --i)
+        if (next > -INFINITY && c[i] == next) e = expert[i];
+      int lowest = e;
+#pragma unroll
+      for (int o = L / 2; o >= 1; o >>= 1) lowest = min(lowest, __shfl_xor_sync(0xffffffffu, lowest, o));
+      const bool found = lowest != 0x7FFFFFFF;
+      if (found && e == lowest) {
 #pragma unroll
         for (int i = 0; i < V; ++i)
-          if (!found && c[i] == next) {
-            found = true;
-            c[i] = -INFINITY;
-            e = tl * V + i;
-          }
+          if (expert[i] == e) c[i] = -INFINITY;
       }
-      e = __shfl_sync(0xffffffffu, e, src < 0 ? 0 : src, L);
+      e = lowest;
       // equal logits with equal biases tie whatever the precision
-      if (BIAS && src >= 0 && before - next <= near &&
+      if (BIAS && found && before - next <= near &&
           !(gate_at(row, e) == gate_at(row, before_e) && __ldg(p.bias + e) == __ldg(p.bias + before_e)))
         close = true;
       before = next;
       before_e = e;
-      if (tl == j && j < p.topk && src >= 0) found_id = e;
+      if (tl == j && j < p.topk && found) found_id = e;
     }
     if (all > kGateList) {
       mine_id = found_id;
@@ -802,10 +846,14 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(cons
       v = p.scale * ((x < 0.0f ? tail : 1.0f) * inv) * rest * g;
     }
   }
+  // whole runs of V experts a lane, or one expert after another
+  const bool vec = p.E % V == 0;
+  const int first = vec ? lane * V : lane, step = vec ? 1 : 32;
+  const int live = vec ? (first < p.E ? V : 0) : max(0, (p.E - lane + 31) / 32);
   float o[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.0f;
-  gate_store_row<V>(acc, 32 * V, lane, o);
+  gate_store_row<V>(acc, lane * V, 1, V, true, o);
   __syncwarp();
   if (has) {
     acc[id] = v;
@@ -821,19 +869,19 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(cons
       __syncwarp();
     }
   }
-  if constexpr (V >= 4) {
+  if (V >= 4 && vec) {
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) {
-      const float4 q = reinterpret_cast<const float4*>(acc + lane * V)[i];
+      const float4 q = reinterpret_cast<const float4*>(acc + first)[i];
       o[4 * i] = q.x, o[4 * i + 1] = q.y, o[4 * i + 2] = q.z, o[4 * i + 3] = q.w;
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = acc[lane * V + i];
+    for (int i = 0; i < V; ++i) o[i] = acc[first + i * step];
   }
   if (dense && __any_sync(0xffffffffu, has)) {
     float l[V];
-    gate_load_row<V>(row, p.E, lane, -INFINITY, l);
+    gate_load_row<V>(row, first, step, live, vec, -INFINITY, l);
     float m = l[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
@@ -857,7 +905,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(cons
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = p.scale * l[i] * (o[i] - mean);
   }
-  gate_store_row<V>(out, p.E, lane, o);
+  gate_store_row<V>(out, first, step, live, vec, o);
 }
 
 }  // namespace dg

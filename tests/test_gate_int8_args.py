@@ -123,6 +123,14 @@ def test_binding_refuses_before_the_library_is_called():
         dg._operand(x, (torch.float32,), (4, 16), "x", 0)
 
 
+def test_operands_of_another_device_than_the_current_one_are_refused(monkeypatch):
+    monkeypatch.setattr(dg, "_current_device", lambda: 1)
+    monkeypatch.setattr(dg, "_current_stream", lambda dev: 7 + dev)
+    assert dg._launch_stream(1) == 8
+    with pytest.raises(ValueError, match="cuda:0 but the current device is cuda:1"):
+        dg._launch_stream(0)
+
+
 def test_int8_tile_choice(lib):
     """The heuristic is host logic (148 SMs assumed without a device): narrow
     1-CTA tiles for a few rows, pairs of CTAs for many, no pairs beyond the

@@ -90,9 +90,12 @@ def test_biased_choice(T, E, topk, score, dtype):
 @pytest.mark.parametrize("score,biased", [("softmax", False), ("sigmoid", True), ("sigmoid", False)])
 @pytest.mark.parametrize("T,E,topk,n_group,topk_group", [
     (300, 256, 8, 8, 4), (40, 64, 4, 4, 2), (100, 160, 6, 8, 3), (50, 60, 4, 6, 2), (30, 256, 8, 32, 3),
-    (20, 1024, 16, 16, 5), (25, 66, 3, 3, 1), (30, 16, 2, 8, 8), (10, 96, 8, 2, 1), (64, 512, 8, 4, 2)])
+    (20, 1024, 16, 16, 5), (25, 66, 3, 3, 1), (30, 16, 2, 8, 8), (10, 96, 8, 2, 1), (64, 512, 8, 4, 2),
+    (21, 1020, 12, 17, 4), (15, 1000, 8, 8, 3), (33, 384, 8, 8, 2), (40, 100, 8, 5, 2), (9, 1024, 32, 32, 3),
+    (13, 93, 7, 31, 9), (11, 992, 8, 31, 6), (50, 36, 12, 6, 3), (8, 1024, 8, 2, 1)])
 def test_groups(T, E, topk, n_group, topk_group, score, biased, group_top):
-    """Groups that are whole lanes of the warp and those that are not."""
+    """Groups whose experts are whole runs of a lane, groups that fill their lanes
+    in part, and (17 and 31 groups of many) groups that share lanes."""
     b = 0.05 * _rand(1, E, 9)[0] if biased else None
     check_gate(_rand(T, E, T + 7 * E), topk, b, score=score, n_group=n_group, topk_group=topk_group,
                group_top=group_top, renormalize=True, scale=2.5)
