@@ -516,17 +516,15 @@ def moe_quantize_permute_int8(topk_ids, num_experts: int, x, out=None):
     ([T, topk]); a / sa / m_indices are the operands of m_grouped_int8_gemm_nt_contiguous.  `out`, if given, is
     such a dict of preallocated tensors (M_cap = dg_moe_permute_capacity).
     """
-    _cuda_matrix(topk_ids, _I32T, "topk_ids")
     _cuda_matrix(x, _BF16_F32, "x")
-    T, topk = topk_ids.shape
-    K = x.shape[1]
-    if x.shape[0] != T:
-        raise ValueError(f"x must be [T, K] with T = {T} rows, one per token of topk_ids")
-    _same_device(x, topk_ids)
+    T, K = x.shape
+    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
+        raise ValueError(f"topk_ids must be [T, topk] with T = {T} rows, one per token of x")
+    topk = topk_ids.shape[1]
     lib = load()
-    cap = lib.dg_moe_permute_capacity(T, topk, num_experts)
-    if cap < 0:
-        _check(cap)
+    cap = (T * topk + 127 * num_experts + 127) // 128 * 128    # dg_moe_permute_capacity
+    if topk <= 0 or num_experts <= 0 or cap > 0x7FFFFFFF:
+        _check(lib.dg_moe_permute_capacity(T, topk, num_experts))
     dev = x.get_device()
     if out is None:
         out = {
@@ -541,7 +539,7 @@ def moe_quantize_permute_int8(topk_ids, num_experts: int, x, out=None):
             if key not in out:
                 raise ValueError(f"out[{key!r}] is missing")
     _check(lib.dg_moe_quantize_permute_int8(
-        topk_ids.data_ptr(), T, topk, num_experts, x.data_ptr(), _FLOAT_CODES[x.dtype], K,
+        _operand(topk_ids, _I32T, (T, topk), "topk_ids", dev), T, topk, num_experts, x.data_ptr(), _FLOAT_CODES[x.dtype], K,
         _operand(out["a"], _INT8, (cap, K), "out['a']", dev), _operand(out["sa"], _F32T, (cap,), "out['sa']", dev),
         _operand(out["m_indices"], _I32T, (cap,), "out['m_indices']", dev),
         _operand(out["row_of"], _I32T, (T, topk), "out['row_of']", dev),

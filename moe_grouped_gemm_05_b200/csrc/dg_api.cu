@@ -892,16 +892,21 @@ static cudaError_t launch_gate(GateArgs& p, cudaStream_t st) {
   if (width <= 16) return launch_gate_v<T, 32, 16>(p, st);
   return launch_gate_v<T, 32, 32>(p, st);
 }
-template <typename T>
-static cudaError_t launch_gate_backward(const GateBackwardArgs& p, cudaStream_t st) {
+template <typename T, int V>
+static cudaError_t launch_gate_backward_v(const GateBackwardArgs& p, cudaStream_t st) {
   const long long blocks = (static_cast<long long>(p.T) + kGateWarps - 1) / kGateWarps;
   constexpr int th = 32 * kGateWarps;
-  if (p.E <= 32) return launch_plain(moe_gate_backward_kernel<T, 1>, blocks, th, st, p);
-  if (p.E <= 64) return launch_plain(moe_gate_backward_kernel<T, 2>, blocks, th, st, p);
-  if (p.E <= 128) return launch_plain(moe_gate_backward_kernel<T, 4>, blocks, th, st, p);
-  if (p.E <= 256) return launch_plain(moe_gate_backward_kernel<T, 8>, blocks, th, st, p);
-  if (p.E <= 512) return launch_plain(moe_gate_backward_kernel<T, 16>, blocks, th, st, p);
-  return launch_plain(moe_gate_backward_kernel<T, 32>, blocks, th, st, p);
+  return p.E % V == 0 ? launch_plain(moe_gate_backward_kernel<T, V, true>, blocks, th, st, p)
+                      : launch_plain(moe_gate_backward_kernel<T, V, false>, blocks, th, st, p);
+}
+template <typename T>
+static cudaError_t launch_gate_backward(const GateBackwardArgs& p, cudaStream_t st) {
+  if (p.E <= 32) return launch_gate_backward_v<T, 1>(p, st);
+  if (p.E <= 64) return launch_gate_backward_v<T, 2>(p, st);
+  if (p.E <= 128) return launch_gate_backward_v<T, 4>(p, st);
+  if (p.E <= 256) return launch_gate_backward_v<T, 8>(p, st);
+  if (p.E <= 512) return launch_gate_backward_v<T, 16>(p, st);
+  return launch_gate_backward_v<T, 32>(p, st);
 }
 
 // ------------------------------------------------------------------ pack kernel

@@ -803,7 +803,8 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
 // memory and written once.  16384 x 256 FP32, topk 8: 6.8 us (2.7 TB/s, the rows
 // coming from L2), dense softmax 7.7 us; bound by the latency of the gathered
 // logits and of the sums, which one row's warp cannot overlap.
-template <typename LT, int V>
+// VEC: E % V == 0, whole runs of V experts a lane; else one expert after another.
+template <typename LT, int V, bool VEC>
 __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(const GateBackwardArgs p) {
   __shared__ __align__(16) float rows[kGateWarps][32 * V];
   __shared__ int owner[kGateWarps][32 * V];
@@ -846,10 +847,9 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(cons
       v = p.scale * ((x < 0.0f ? tail : 1.0f) * inv) * rest * g;
     }
   }
-  // whole runs of V experts a lane, or one expert after another
-  const bool vec = p.E % V == 0;
-  const int first = vec ? lane * V : lane, step = vec ? 1 : 32;
-  const int live = vec ? (first < p.E ? V : 0) : max(0, (p.E - lane + 31) / 32);
+  const int first = VEC ? lane * V : lane;
+  constexpr int step = VEC ? 1 : 32;
+  const int live = VEC ? (first < p.E ? V : 0) : max(0, (p.E - lane + 31) / 32);
   float o[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) o[i] = 0.0f;
@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(cons
       __syncwarp();
     }
   }
-  if (V >= 4 && vec) {
+  if constexpr (V >= 4 && VEC) {
 #pragma unroll
     for (int i = 0; i < V / 4; ++i) {
       const float4 q = reinterpret_cast<const float4*>(acc + first)[i];
@@ -881,7 +881,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(cons
   }
   if (dense && __any_sync(0xffffffffu, has)) {
     float l[V];
-    gate_load_row<V>(row, first, step, live, vec, -INFINITY, l);
+    gate_load_row<V>(row, first, step, live, VEC, -INFINITY, l);
     float m = l[0];
 #pragma unroll
     for (int i = 1; i < V; ++i) m = fmaxf(m, l[i]);
@@ -905,7 +905,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_backward_kernel(cons
 #pragma unroll
     for (int i = 0; i < V; ++i) o[i] = p.scale * l[i] * (o[i] - mean);
   }
-  gate_store_row<V>(out, first, step, live, vec, o);
+  gate_store_row<V>(out, first, step, live, VEC, o);
 }
 
 }  // namespace dg

@@ -109,7 +109,7 @@ def test_binding_refuses_before_the_library_is_called():
         dg.quantize_int8_per_token(x)
     with pytest.raises(TypeError, match="int8"):
         dg.int8_gemm_nt(x, x, x, x)
-    with pytest.raises(TypeError, match="int32"):
+    with pytest.raises(ValueError, match="CUDA"):
         dg.moe_quantize_permute_int8(x, 4, x)
     cpu = -1      # the device number of CPU tensors
     assert dg._operand(x, (torch.float32,), (4, 16), "x", cpu) == x.data_ptr()

@@ -506,3 +506,30 @@ def test_gate_feeds_the_fp8_chain():
     assert np.array_equal(per["row_of"].cpu().numpy(), row_of)
     check_close(bits(out), oracle.fp8_gemm.moe_unpermute_combine(bits(d), row_of, ref_w.astype(np.float32)), "combine")
     assert dg.get_device_error() == 0
+
+
+def test_wrong_operands_are_refused_before_a_launch():
+    x = torch.zeros((4, 64), device="cuda")
+    ids = torch.zeros((4, 2), dtype=torch.int32, device="cuda")
+    a, s = torch.zeros((4, 64), dtype=torch.int8, device="cuda"), torch.ones(4, device="cuda")
+    with pytest.raises(ValueError, match="topk_ids"):
+        dg.moe_quantize_permute_int8(ids[:3], 4, x)
+    with pytest.raises(TypeError, match="topk_ids"):
+        dg.moe_quantize_permute_int8(ids.long(), 4, x)
+    with pytest.raises(dg.DGError):
+        dg.moe_quantize_permute_int8(ids, 0, x)
+    with pytest.raises(dg.DGError):
+        dg.moe_quantize_permute_int8(ids, 2000, x)
+    with pytest.raises(ValueError, match="sa"):
+        dg.int8_gemm_nt(a, s[:3], a, s)
+    with pytest.raises(ValueError, match="b must"):
+        dg.int8_gemm_nt(a, s, torch.zeros((16, 32), dtype=torch.int8, device="cuda"), torch.ones(16, device="cuda"))
+    with pytest.raises(dg.DGError, match="multiple of 16"):
+        dg.int8_gemm_nt(a, s, a, s)                       # N = 4
+    with pytest.raises(ValueError, match="contiguous"):
+        dg.quantize_int8_per_token(x.t())
+    with pytest.raises(dg.DGError, match="aligned"):
+        dg.quantize_int8_per_token(torch.zeros(4 * 64 + 1, device="cuda")[1:].reshape(4, 64))
+    with pytest.raises(dg.DGError, match="topk"):
+        dg.moe_gate(x, 65)
+    assert dg.get_device_error() == 0
