@@ -858,7 +858,8 @@ static cudaError_t launch_gate_v(GateArgs& p, cudaStream_t st) {
   p.span_log2 = -1;
   if (p.n_group > 1 && p.width <= V)
     for (p.span_log2 = 0; (1 << p.span_log2) < span;) ++p.span_log2;
-  p.vec = p.span_log2 >= 0 ? p.width == V && p.gsize % V == 0 : p.E % V == 0;
+  // whole runs; with groups, lane tl's is the tl-th of the row only where every group fills its lanes
+  p.vec = p.span_log2 >= 0 ? p.gsize == span * V : p.E % V == 0;
   p.full = p.vec && p.E == L * V;
   p.deal = p.span_log2 >= 0 && p.topk_group * span < 2 * p.topk;
   constexpr int th = 32 * kGateWarps, per = th / L;

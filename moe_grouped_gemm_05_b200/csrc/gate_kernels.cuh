@@ -434,8 +434,8 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
   const bool scored = BIAS || sums;
   // This lane's experts.  With groups, each group has lanes of its own (where its
   // experts fit into them); without, a row of whole runs of V is cut into those,
-  // and any other is dealt out an expert at a time.  (Whole runs come out as the
-  // first line has them in both ways.)
+  // and any other is dealt out an expert at a time.  (vec: the first line has it in
+  // both ways, since groups then fill their lanes.)
   int first = tl * V, step = 1, live = first < p.E ? V : 0;
   if (!p.vec) {
     if (p.n_group == 1) {

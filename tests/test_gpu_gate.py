@@ -103,6 +103,20 @@ def test_groups(T, E, topk, n_group, topk_group, score, biased, group_top):
                group_top=group_top)
 
 
+@pytest.mark.parametrize("n_group", [2, 3, 4, 5, 7, 8, 12, 16, 17, 24, 32])
+def test_groups_of_every_size(n_group):
+    """Every group size up to 34 and those around the lanes' runs beyond it: groups that
+    fill their lanes, that leave the last lane in part, and that leave lanes empty."""
+    sizes = [g for g in [*range(1, 35), 42, 52, 56, 60, 112, 120, 127, 128, 224, 240, 496] if g * n_group <= 1024]
+    for gsize in sizes:
+        E, topk_group = gsize * n_group, (n_group + 1) // 2
+        b = 0.05 * _rand(1, E, gsize)[0]
+        few, many = min(4, topk_group * gsize), min(32, topk_group * gsize)
+        check_gate(_rand(4, E, E), few, b, score="sigmoid", n_group=n_group, topk_group=topk_group,
+                   group_top=min(2, gsize))
+        check_gate(_rand(4, E, E + 1, torch.bfloat16), many, n_group=n_group, topk_group=topk_group)
+
+
 def test_large_batch_and_ragged_tail():
     check_gate(_rand(20001, 64, 3, torch.bfloat16), 6, score="softmax", renormalize=True)
     check_gate(_rand(4099, 256, 4), 8, 0.05 * _rand(1, 256, 6)[0], score="sigmoid", n_group=8, topk_group=4,
