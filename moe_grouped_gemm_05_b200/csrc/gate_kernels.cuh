@@ -281,17 +281,21 @@ __device__ __forceinline__ void merge_top2(R& a1, R& a2, R b1, R b2) {
 
 // A group's score from its two best values: the best, or the sum of both (of
 // one where only one expert of the group can be chosen); -inf where none can.
-template <typename R>
-__device__ __forceinline__ R group_score(R a1, R a2, int group_top) {
-  return group_top == 1 || a2 == -INFINITY ? a1 : a1 + a2;
+// A sum beyond the type's range is its largest value, so that a group of two
+// experts with the lowest bias can still be kept.
+__device__ __forceinline__ float group_score(float a1, float a2, int group_top) {
+  return group_top == 1 || a2 == -INFINITY ? a1 : fminf(fmaxf(a1 + a2, -FLT_MAX), FLT_MAX);
+}
+__device__ __forceinline__ double group_score(double a1, double a2, int group_top) {
+  return group_top == 1 || a2 == -INFINITY ? a1 : a1 + a2;  // (of 32-bit biases: within range)
 }
 
-// Scores of all groups for any group size: lane g of the team gets group g's
-// (-inf behind the last).  v: the lane's V values, -inf where an expert cannot
-// be chosen.
+// The two best values of each group for any group size: lane g of the team gets
+// group g's in m1 >= m2 (-inf behind the last).  v: the lane's V values, -inf
+// where an expert cannot be chosen.
 template <typename R, int L, int V>
-__device__ __forceinline__ R group_scores_any(const R (&v)[V], int tl, int n_group, int gsize, int group_top) {
-  R mine = -INFINITY;
+__device__ __forceinline__ void group_best_any(const R (&v)[V], int tl, int n_group, int gsize, R& m1, R& m2) {
+  m1 = m2 = -INFINITY;
   for (int g = 0; g < n_group; ++g) {
     R a1 = -INFINITY, a2 = -INFINITY;
 #pragma unroll
@@ -304,9 +308,11 @@ __device__ __forceinline__ R group_scores_any(const R (&v)[V], int tl, int n_gro
       const R b1 = __shfl_xor_sync(0xffffffffu, a1, o), b2 = __shfl_xor_sync(0xffffffffu, a2, o);
       merge_top2(a1, a2, b1, b2);
     }
-    if (tl == g) mine = group_score(a1, a2, group_top);
+    if (tl == g) {
+      m1 = a1;
+      m2 = a2;
+    }
   }
-  return mine;
 }
 
 // ---------------------------------------------------------------- the choice in 64 bits
@@ -345,7 +351,9 @@ __device__ __noinline__ int gate_choose64(const GateArgs& p, const LT* row, int 
     k[i] = p.bias || dead ? c[i] : x;  // without a bias the experts go by their logits
   }
   if (p.n_group > 1) {
-    const double mine = group_scores_any<double, L, V>(c, tl, p.n_group, p.gsize, p.group_top);
+    double m1, m2;
+    group_best_any<double, L, V>(c, tl, p.n_group, p.gsize, m1, m2);
+    const double mine = group_score(m1, m2, p.group_top);
     int rank = 0;
     for (int j = 0; j < p.n_group; ++j) {
       const double o = __shfl_sync(0xffffffffu, mine, j, L);
@@ -394,14 +402,18 @@ __device__ __noinline__ int gate_choose64(const GateArgs& p, const LT* row, int 
 //   softmax  p |x| 2u <= 0.74u and 4u p from the exponential; from the sum (at
 //            most 1024 terms, in 64 bits (2 + 2 * 6.94) u of their own and 37 u
 //            of additions) and the quotient 60u p: <= p 2^-17 + u.
-// c = s + b adds |c| u <= (1 + B) u, B the largest |b|.  Two values closer than
-// both errors together (`near`) are not told apart; a sum of two has both
-// terms' errors and its own rounding, 2 (1 + B) u.
+// That is `e0`.  c = s + b adds |c| u, and at most 1, since b itself lies within 1 of
+// s + b: a bias of any size, the type's lowest among them, leaves values at a distance
+// told apart.  Values a < k can be out of order only where k - a is at most both errors
+// together, and then |a| <= |k| + (k - a): so within `gate_near` of k, which k alone
+// decides.  A sum of two has both terms' errors and its own, at most u |sum| and at
+// most the smaller term (the larger one is a 32-bit number too; so with the sum cut off
+// at the type's range).
 //
 // The choice.  The topk-th largest of the lanes' best values is a lower bound
 // of the topk-th best value of the row, since so many values reach it, and few
 // values do (for 256 experts, topk 8: about eleven).  Those (and the ones
-// closer below it than `near`) are put together in shared memory, and each
+// within `gate_near` below it) are put together in shared memory, and each
 // lane counts the ones before its own.  That takes the place of topk rounds of
 // finding and removing the best (which serve the rows with more than 32).
 //
@@ -411,6 +423,18 @@ __device__ __noinline__ int gate_choose64(const GateArgs& p, const LT* row, int 
 // before groups of any size had lanes of their own and few kept experts were dealt
 // out).  Bound by issue, some 710 instructions a token of 256 experts; more resident
 // warps or larger blocks change nothing.
+__device__ __forceinline__ float gate_near(float e0, float k) {
+  return 2.0f * e0 + fminf(0x1.001p-23f * (1.0f + fabsf(k)), 3.0f);
+}
+// Error of a group's score, made of a1 or of a1 >= a2.
+__device__ __forceinline__ float group_error(float e0, float a1, float a2, int group_top) {
+  constexpr float u = 0x1.001p-24f;
+  const float x1 = fabsf(a1), x2 = fabsf(a2), err = e0 + fminf(u * x1, 1.0f);
+  if (group_top == 1 || a2 == -INFINITY) return err;
+  const float sum = fabsf(a1 + a2);
+  return err + e0 + fminf(u * x2, 1.0f) + fminf(sum < INFINITY ? u * sum : INFINITY, fminf(x1, x2));
+}
+
 template <typename LT, int L, int V, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_constant__ GateArgs p) {
   constexpr int kTeams = 32 * kGateWarps / L;
@@ -471,7 +495,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
     for (int i = 0; i < V; ++i) sum += i < live ? expf(l[i] - top) : 0.0f;
     total = team_sum<L>(sum);
   }
-  float near = 0.0f;
+  float e0 = 0.0f;
   if (scored) {
     const float inv = SIGMOID ? 1.0f : fast_rcp(total);
 #pragma unroll
@@ -479,7 +503,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       const float s = SIGMOID ? fast_rcp(1.0f + fast_exp2(-kLog2e * l[i])) : fast_exp2(kLog2e * (l[i] - top)) * inv;
       c[i] = BIAS ? s + c[i] : s;
     }
-    near = 0x1.4p-21f + (SIGMOID ? 0.0f : 0x1p-16f * inv);  // 10u
+    e0 = 0x1.4p-22f + (SIGMOID ? 0.0f : 0x1p-17f * inv);  // 5u
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) c[i] = l[i];
@@ -495,7 +519,6 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
         const float b = i < live ? __ldg(p.bias + first + i * step) : 0.0f;
         bad |= !(b < INFINITY);
         if (b == -INFINITY) c[i] = -INFINITY;
-        largest = fmaxf(i == 0 ? 0.0f : largest, b > -INFINITY ? fabsf(b) : 0.0f);
       }
     }
     if (team_any<L>(bad, lane)) {
@@ -503,12 +526,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       if (tl == 0) atomicOr(&g_dg_error, 0x20);
 #pragma unroll
       for (int i = 0; i < V; ++i) c[i] = -INFINITY;
-      largest = 0.0f;
     }
-  }
-  if (BIAS) {
-    largest = team_max<L>(largest);
-    near += 0x1p-23f * (1.0f + largest);
   }
   if (!p.full) {
 #pragma unroll
@@ -524,8 +542,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
     const bool whole = p.span_log2 >= 0;
     const int span = whole ? 1 << p.span_log2 : 1;
     const int at = whole ? tl >> p.span_log2 : tl;  // the group whose score this lane holds
-    float mine;
-    float a1 = c[0], a2 = -INFINITY;
+    float a1 = c[0], a2 = -INFINITY;  // the group's two best values
     if (whole) {
 #pragma unroll
       for (int i = 1; i < V; ++i) {
@@ -537,13 +554,17 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
         a2 = fmaxf(fminf(a1, b1), fmaxf(a2, b2));
         a1 = fmaxf(a1, b1);
       }
-      mine = group_score(a1, a2, p.group_top);
     } else {
-      mine = group_scores_any<float, L, V>(c, tl, p.n_group, p.gsize, p.group_top);
+      group_best_any<float, L, V>(c, tl, p.n_group, p.gsize, a1, a2);
     }
+    const float mine = group_score(a1, a2, p.group_top);
     // lanes behind the last group have -inf, as groups without an expert to choose
     const bool some = mine > -INFINITY;
-    const float gnear = scored ? 2.0f * near + 0x1p-21f * (1.0f + largest) : 0.0f;
+    float gerr = 0.0f, gnear = 0.0f;  // the score's error, and twice the largest
+    if (scored) {
+      gerr = some ? group_error(e0, a1, a2, p.group_top) : 0.0f;
+      gnear = 2.0f * team_max<L>(gerr);
+    }
     // the topk_group-th best score, and the best below it
     const float kth = team_kth<L>(mine, L == 32 ? p.topk_group : p.topk_group * span, lane);
     bool kept = some && mine >= kth;
@@ -557,9 +578,10 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       int above = 0, sure_above = 0, maybe_above = 0;
       for (int j = 0; j < p.n_group; ++j) {
         const float o = __shfl_sync(0xffffffffu, mine, j * span, L);
+        const float both = gerr + __shfl_sync(0xffffffffu, gerr, j * span, L);
         above += o > mine || (o == mine && j < at);
-        sure_above += o > mine + gnear;
-        maybe_above += j != at && o >= mine - gnear;
+        sure_above += o - mine > both;
+        maybe_above += j != at && mine - o <= both;
       }
       if (slow) kept = some && above < p.topk_group;
       // is a kept group too close to one that is not?
@@ -567,7 +589,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       if (__any_sync(0xffffffffu, unsure) && whole) {
         // The groups' scores in 64 bits, from the one or two experts that each
         // is made of, if 32 bits tell those from the group's others.
-        const float lowest = (p.group_top == 1 || a2 == -INFINITY ? a1 : a2) - near;
+        const float least = p.group_top == 1 || a2 == -INFINITY ? a1 : a2, lowest = least - gate_near(e0, least);
         int n = 0, e1 = -1, e2 = -1;
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -647,7 +669,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
   if (tl == 0) *count = 0;
   const float kth = team_kth<L>(best, p.topk, lane);
   // (-FLT_MAX where fewer lanes than topk have an expert: every one is in question)
-  const float bound = kth == -INFINITY ? -FLT_MAX : BIAS ? kth - near : kth;
+  const float bound = kth == -INFINITY ? -FLT_MAX : BIAS ? kth - gate_near(e0, kth) : kth;
   int n = 0;
 #pragma unroll
   for (int i = 0; i < V; ++i) count_from(n, c[i], bound);
@@ -700,7 +722,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
   mine_id = tl < p.topk ? __float_as_int(y.y) : -1;
   if (BIAS) {
     // neighbours in the order, down to the first behind the chosen ones
-    const bool near_one = tl < p.topk && tl + 1 < m && y.x - list[tl + 1].x <= near;
+    const bool near_one = tl < p.topk && tl + 1 < m && y.x - list[tl + 1].x <= gate_near(e0, y.x);
     if (__any_sync(0xffffffffu, near_one)) {
       const bool found_near = team_any<L>(near_one, lane);
       const bool redo = found_near && all <= kGateList;
@@ -757,7 +779,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
       }
       e = lowest;
       // equal logits with equal biases tie whatever the precision
-      if (BIAS && found && before - next <= near &&
+      if (BIAS && found && before - next <= gate_near(e0, before) &&
           !(gate_at(row, e) == gate_at(row, before_e) && __ldg(p.bias + e) == __ldg(p.bias + before_e)))
         close = true;
       before = next;

@@ -187,6 +187,29 @@ def test_masks_and_padding():
     assert (ids == -1).all() and (w == 0).all()
 
 
+@pytest.mark.parametrize("T,E,topk,n_group,topk_group", [
+    (5, 20, 6, 1, 1), (7, 24, 10, 4, 2), (9, 33, 20, 3, 2), (6, 60, 6, 6, 2), (12, 64, 8, 1, 1), (8, 256, 8, 8, 4),
+    (5, 160, 6, 8, 3), (4, 1000, 16, 8, 3), (4, 1020, 12, 17, 4), (6, 32, 32, 1, 1), (11, 100, 32, 5, 4)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_of_any_size(T, E, topk, n_group, topk_group, score):
+    """Biases that push experts out of the choice without masking them (the type's lowest
+    value, -1e9, -1e4), for fewer and for more experts than leave the slots filled, and
+    biases in whose last place every score is lost."""
+    lowest = torch.finfo(torch.float32).min
+    rng = np.random.default_rng(E)
+    l = _rand(T, E, E + 3)
+    l[1, ::3] = -INF
+    kw = dict(score=score, n_group=n_group, topk_group=topk_group)
+    for value in (lowest, -1e9, -1e4, -2.0 ** 24, lowest / 2, 2.0 ** 23, 3e38):
+        for share in (0.1, 0.5, 0.9, 1.0):
+            b = 0.05 * _rand(1, E, 5)[0]
+            b[torch.from_numpy(rng.random(E) < share)] = value
+            for group_top in {1, min(2, E // n_group)}:
+                check_gate(l, topk, b, group_top=group_top, **kw)
+    b = torch.tensor([lowest, -lowest, 0.0, -INF])[torch.from_numpy(rng.integers(0, 4, E))]
+    check_gate(l, topk, b, group_top=min(2, E // n_group), **kw)
+
+
 @pytest.mark.parametrize("what", [float("nan"), INF])
 def test_rows_that_are_not_numbers_are_not_routed(what):
     l = _rand(10, 60, 41)
