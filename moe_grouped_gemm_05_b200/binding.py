@@ -426,6 +426,7 @@ def _operand(t, dtypes, shape, name: str, dev: int) -> int:
     return t.data_ptr()
 
 
+_INT_MAX = 0x7FFFFFFF
 _FLOAT_CODES = {torch.bfloat16: 0, torch.float32: 1}
 _INT8, _I32T, _F32T, _BF16T = (torch.int8,), (torch.int32,), (torch.float32,), (torch.bfloat16,)
 _BF16_F32 = (torch.bfloat16, torch.float32)
@@ -453,6 +454,8 @@ def moe_gate(logits, topk: int, bias=None, *, score: str = "softmax", n_group: i
         raise ValueError(f"unknown score {score!r}: softmax or sigmoid")
     _cuda_matrix(logits, _BF16_F32, "logits")
     T, E = logits.shape
+    if max(T, n_group, topk_group, group_top) > _INT_MAX:     # ctypes would take them modulo 2^32
+        raise ValueError(f"{T} tokens, n_group={n_group}, topk_group={topk_group}, group_top={group_top}: beyond 32 bits")
     dev = logits.get_device()
     if ids is None:
         ids = torch.empty((T, max(0, topk)), dtype=torch.int32, device=logits.device)
@@ -478,6 +481,8 @@ def moe_gate_backward(logits, topk_ids, d_weights, *, score: str = "softmax", re
     _cuda_matrix(logits, _BF16_F32, "logits")
     _cuda_matrix(topk_ids, _I32T, "topk_ids")
     T, E = logits.shape
+    if T > _INT_MAX:
+        raise ValueError(f"{T} tokens: beyond 32 bits")
     topk = topk_ids.shape[1]
     dev = logits.get_device()
     if d_logits is None:
@@ -523,7 +528,7 @@ def moe_quantize_permute_int8(topk_ids, num_experts: int, x, out=None):
     topk = topk_ids.shape[1]
     lib = load()
     cap = (T * topk + 127 * num_experts + 127) // 128 * 128    # dg_moe_permute_capacity
-    if topk <= 0 or num_experts <= 0 or cap > 0x7FFFFFFF:
+    if topk <= 0 or num_experts <= 0 or cap > _INT_MAX:
         _check(lib.dg_moe_permute_capacity(T, topk, num_experts))
     dev = x.get_device()
     if out is None:

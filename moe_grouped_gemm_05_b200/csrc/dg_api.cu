@@ -822,7 +822,7 @@ static cudaError_t launch_quantize_int8(const QuantArgs& p, cudaStream_t st) {
                      : &quantize_int8_kernel<T, 0, PERM>;
   LaunchAttrs la(1);
   cudaLaunchConfig_t lc = {};
-  lc.gridDim = dim3((p.M + teams - 1) / teams);
+  lc.gridDim = dim3(p.M / teams + (p.M % teams != 0));
   lc.blockDim = dim3(32, warps, teams);
   lc.stream = st;
   lc.attrs = la.attr;

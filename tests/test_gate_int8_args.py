@@ -123,6 +123,19 @@ def test_binding_refuses_before_the_library_is_called():
         dg._operand(x, (torch.float32,), (4, 16), "x", 0)
 
 
+def test_sizes_beyond_32_bits_are_refused(monkeypatch):
+    """The library takes C ints: 2^32 + 5 tokens must not become 5."""
+    monkeypatch.setattr(dg, "_cuda_matrix", lambda *args: None)
+    many = torch.empty((2 ** 32 + 5, 1), device="meta")
+    with pytest.raises(ValueError, match="32 bits"):
+        dg.moe_gate(many, 1)
+    with pytest.raises(ValueError, match="32 bits"):
+        dg.moe_gate_backward(many, many.to(torch.int32), many)
+    for name in ("n_group", "topk_group", "group_top"):
+        with pytest.raises(ValueError, match="32 bits"):
+            dg.moe_gate(torch.zeros(4, 16), 2, **{name: 2 ** 32 + 1})
+
+
 def test_operands_of_another_device_than_the_current_one_are_refused(monkeypatch):
     monkeypatch.setattr(dg, "_current_device", lambda: 1)
     monkeypatch.setattr(dg, "_current_stream", lambda dev: 7 + dev)
