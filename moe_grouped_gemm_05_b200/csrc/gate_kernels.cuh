@@ -560,11 +560,9 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
     const float mine = group_score(a1, a2, p.group_top);
     // lanes behind the last group have -inf, as groups without an expert to choose
     const bool some = mine > -INFINITY;
-    float gerr = 0.0f, gnear = 0.0f;  // the score's error, and twice the largest
-    if (scored) {
-      gerr = some ? group_error(e0, a1, a2, p.group_top) : 0.0f;
-      gnear = 2.0f * team_max<L>(gerr);
-    }
+    // no less than twice the largest group_error, in fewer steps
+    const float gnear =
+        scored ? 4.0f * e0 + 0x1.01p-22f * team_max<L>(some ? fabsf(a1) + fabsf(a2) : 0.0f) : 0.0f;
     // the topk_group-th best score, and the best below it
     const float kth = team_kth<L>(mine, L == 32 ? p.topk_group : p.topk_group * span, lane);
     bool kept = some && mine >= kth;
@@ -575,6 +573,7 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
                       lanes_kept > p.topk_group * span;
     if (__any_sync(0xffffffffu, slow)) {
       // a close call, or equal scores: rank the groups one by one
+      const float gerr = scored && some ? group_error(e0, a1, a2, p.group_top) : 0.0f;
       int above = 0, sure_above = 0, maybe_above = 0;
       for (int j = 0; j < p.n_group; ++j) {
         const float o = __shfl_sync(0xffffffffu, mine, j * span, L);
