@@ -420,7 +420,7 @@ def _operand(t, dtypes, shape, name: str, dev: int) -> int:
     """Checks one operand (dtype, shape, contiguity, device number) and returns its address."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+    if t.shape != shape or t.get_device() != dev or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous tensor of shape {tuple(shape)} on cuda:{dev}, got shape "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -433,11 +433,13 @@ _BF16_F32 = (torch.bfloat16, torch.float32)
 
 
 def _cuda_matrix(t, dtypes, name: str, dims: int = 2):
-    """Checks the leading operand of a call: its dtype, rank, and that it is a contiguous CUDA tensor."""
+    """Checks the leading operand of a call (dtype, rank, a contiguous CUDA tensor); returns its shape and device."""
     if t.dtype not in dtypes:
         raise TypeError(f"{name} must be {' or '.join(str(d) for d in dtypes)}, got {t.dtype}")
-    if not t.is_cuda or not t.is_contiguous() or t.dim() != dims:
+    shape, dev = t.shape, t.get_device()     # -1: the CPU
+    if dev < 0 or len(shape) != dims or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor of {dims} dimensions")
+    return shape, dev
 
 
 def moe_gate(logits, topk: int, bias=None, *, score: str = "softmax", n_group: int = 1, topk_group: int = 1,
@@ -452,11 +454,9 @@ def moe_gate(logits, topk: int, bias=None, *, score: str = "softmax", n_group: i
     """
     if score not in _SCORES:
         raise ValueError(f"unknown score {score!r}: softmax or sigmoid")
-    _cuda_matrix(logits, _BF16_F32, "logits")
-    T, E = logits.shape
+    (T, E), dev = _cuda_matrix(logits, _BF16_F32, "logits")
     if max(T, n_group, topk_group, group_top) > _INT_MAX:     # ctypes would take them modulo 2^32
         raise ValueError(f"{T} tokens, n_group={n_group}, topk_group={topk_group}, group_top={group_top}: beyond 32 bits")
-    dev = logits.get_device()
     if ids is None:
         ids = torch.empty((T, max(0, topk)), dtype=torch.int32, device=logits.device)
     if weights is None:
@@ -478,13 +478,10 @@ def moe_gate_backward(logits, topk_ids, d_weights, *, score: str = "softmax", re
     """
     if score not in _SCORES:
         raise ValueError(f"unknown score {score!r}: softmax or sigmoid")
-    _cuda_matrix(logits, _BF16_F32, "logits")
-    _cuda_matrix(topk_ids, _I32T, "topk_ids")
-    T, E = logits.shape
+    (T, E), dev = _cuda_matrix(logits, _BF16_F32, "logits")
     if T > _INT_MAX:
         raise ValueError(f"{T} tokens: beyond 32 bits")
-    topk = topk_ids.shape[1]
-    dev = logits.get_device()
+    topk = topk_ids.shape[-1] if topk_ids.dim() else 0
     if d_logits is None:
         d_logits = torch.empty_like(logits)
     _check(load().dg_moe_gate_backward(logits.data_ptr(), _FLOAT_CODES[logits.dtype],
@@ -501,14 +498,13 @@ def quantize_int8_per_token(x, q=None, scale=None):
 
     With x [M, K] (or [G, M_max, K]) these are the `a` / `sa` operands of the int8 products.
     """
-    _cuda_matrix(x, _BF16_F32, "x", max(1, x.dim()))
-    lead, K = x.shape[:-1], x.shape[-1]
-    dev = x.get_device()
+    shape, dev = _cuda_matrix(x, _BF16_F32, "x", max(1, x.dim()))
+    lead, K = shape[:-1], shape[-1]
     if q is None:
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
+        q = torch.empty(shape, dtype=torch.int8, device=x.device)
     if scale is None:
         scale = torch.empty(lead, dtype=torch.float32, device=x.device)
-    qp, sp = _operand(q, _INT8, x.shape, "q", dev), _operand(scale, _F32T, lead, "scale", dev)
+    qp, sp = _operand(q, _INT8, shape, "q", dev), _operand(scale, _F32T, lead, "scale", dev)
     _check(load().dg_quantize_int8_per_token(x.data_ptr(), _FLOAT_CODES[x.dtype], qp, sp, lead.numel(), K,
                                              _launch_stream(dev)))
     return q, scale
@@ -521,16 +517,15 @@ def moe_quantize_permute_int8(topk_ids, num_experts: int, x, out=None):
     ([T, topk]); a / sa / m_indices are the operands of m_grouped_int8_gemm_nt_contiguous.  `out`, if given, is
     such a dict of preallocated tensors (M_cap = dg_moe_permute_capacity).
     """
-    _cuda_matrix(x, _BF16_F32, "x")
-    T, K = x.shape
-    if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
+    (T, K), dev = _cuda_matrix(x, _BF16_F32, "x")
+    routed = topk_ids.shape
+    if len(routed) != 2 or routed[0] != T:
         raise ValueError(f"topk_ids must be [T, topk] with T = {T} rows, one per token of x")
-    topk = topk_ids.shape[1]
+    topk = routed[1]
     lib = load()
     cap = (T * topk + 127 * num_experts + 127) // 128 * 128    # dg_moe_permute_capacity
     if topk <= 0 or num_experts <= 0 or cap > _INT_MAX:
         _check(lib.dg_moe_permute_capacity(T, topk, num_experts))
-    dev = x.get_device()
     if out is None:
         out = {
             "a": torch.empty((cap, K), dtype=torch.int8, device=x.device),
@@ -539,16 +534,17 @@ def moe_quantize_permute_int8(topk_ids, num_experts: int, x, out=None):
             "src_of": torch.empty((cap,), dtype=torch.int32, device=x.device),
             "row_of": torch.empty((T, topk), dtype=torch.int32, device=x.device),
         }
-    else:
-        for key in ("a", "sa", "m_indices", "src_of", "row_of"):
-            if key not in out:
-                raise ValueError(f"out[{key!r}] is missing")
+    try:
+        a, sa, m_indices, src_of, row_of = out["a"], out["sa"], out["m_indices"], out["src_of"], out["row_of"]
+    except KeyError as key:
+        raise ValueError(f"out[{key}] is missing") from None
+    rows = (cap,)
     _check(lib.dg_moe_quantize_permute_int8(
-        _operand(topk_ids, _I32T, (T, topk), "topk_ids", dev), T, topk, num_experts, x.data_ptr(), _FLOAT_CODES[x.dtype], K,
-        _operand(out["a"], _INT8, (cap, K), "out['a']", dev), _operand(out["sa"], _F32T, (cap,), "out['sa']", dev),
-        _operand(out["m_indices"], _I32T, (cap,), "out['m_indices']", dev),
-        _operand(out["row_of"], _I32T, (T, topk), "out['row_of']", dev),
-        _operand(out["src_of"], _I32T, (cap,), "out['src_of']", dev), cap, _launch_stream(dev)))
+        _operand(topk_ids, _I32T, routed, "topk_ids", dev), T, topk, num_experts, x.data_ptr(), _FLOAT_CODES[x.dtype], K,
+        _operand(a, _INT8, (cap, K), "out['a']", dev), _operand(sa, _F32T, rows, "out['sa']", dev),
+        _operand(m_indices, _I32T, rows, "out['m_indices']", dev),
+        _operand(row_of, _I32T, routed, "out['row_of']", dev),
+        _operand(src_of, _I32T, rows, "out['src_of']", dev), cap, _launch_stream(dev)))
     return out
 
 
@@ -558,10 +554,8 @@ def int8_gemm_nt(a, sa, b, sb, d=None, out_dtype=torch.bfloat16) -> torch.Tensor
     sa: float32 [M], one scale per token; sb: float32 [N], one per output channel.  D is bf16, or float32 with
     out_dtype=torch.float32 (or a float32 d).
     """
-    _cuda_matrix(a, _INT8, "a")
-    M, K = a.shape
+    (M, K), dev = _cuda_matrix(a, _INT8, "a")
     N = b.shape[0]
-    dev = a.get_device()
     if d is None:
         if out_dtype not in _BF16_F32:
             raise ValueError("out_dtype must be bfloat16 or float32")
@@ -576,11 +570,8 @@ def int8_gemm_nt(a, sa, b, sb, d=None, out_dtype=torch.bfloat16) -> torch.Tensor
 def m_grouped_int8_gemm_nt_contiguous(a, sa, b, sb, m_indices, d=None) -> torch.Tensor:
     """Contiguous-layout grouped int8 GEMM: D[m] = sa[m] * sb[g] * (A[m] . B[g]^T), g = m_indices[m]; -1 rows
     untouched.  a int8 [M_total, K], sa float32 [M_total], b int8 [G, N, K], sb float32 [G, N], D bf16."""
-    _cuda_matrix(a, _INT8, "a")
-    _cuda_matrix(b, _INT8, "b", 3)
-    M, K = a.shape
-    G, N, _ = b.shape
-    dev = a.get_device()
+    (M, K), dev = _cuda_matrix(a, _INT8, "a")
+    (G, N, _), _ = _cuda_matrix(b, _INT8, "b", 3)
     if d is None:
         d = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
     _check(load().dg_m_grouped_int8_gemm_nt_contiguous(
@@ -594,11 +585,8 @@ def m_grouped_int8_gemm_nt_masked(a, sa, b, sb, masked_m, d=None) -> torch.Tenso
     """Masked-layout grouped int8 GEMM: rows m < masked_m[g] of expert g; other rows untouched.
 
     a int8 [G, M_max, K], sa float32 [G, M_max], b int8 [G, N, K], sb float32 [G, N], D bf16 [G, M_max, N]."""
-    _cuda_matrix(a, _INT8, "a", 3)
-    _cuda_matrix(b, _INT8, "b", 3)
-    G, M_max, K = a.shape
-    N = b.shape[1]
-    dev = a.get_device()
+    (G, M_max, K), dev = _cuda_matrix(a, _INT8, "a", 3)
+    (_, N, _), _ = _cuda_matrix(b, _INT8, "b", 3)
     if d is None:
         d = torch.empty((G, M_max, N), dtype=torch.bfloat16, device=a.device)
     _check(load().dg_m_grouped_int8_gemm_nt_masked(

@@ -125,7 +125,7 @@ def test_binding_refuses_before_the_library_is_called():
 
 def test_sizes_beyond_32_bits_are_refused(monkeypatch):
     """The library takes C ints: 2^32 + 5 tokens must not become 5."""
-    monkeypatch.setattr(dg, "_cuda_matrix", lambda *args: None)
+    monkeypatch.setattr(dg, "_cuda_matrix", lambda t, *args: (t.shape, 0))
     many = torch.empty((2 ** 32 + 5, 1), device="meta")
     with pytest.raises(ValueError, match="32 bits"):
         dg.moe_gate(many, 1)
