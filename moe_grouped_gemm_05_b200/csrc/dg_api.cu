@@ -873,7 +873,8 @@ static cudaError_t launch_gate_v(GateArgs& p, cudaStream_t st) {
 // Half a warp a token for up to 128 experts, where its 16 lanes hold the slots and
 // groups and the kernel's list stays short: at most half as many slots as lanes, or
 // no more than 32 experts in the kept groups.  Measured at 16384 tokens: 64 experts,
-// topk 6 6.2 us (a whole warp: 9.4), 128 experts, topk 8 with a bias 9.4 us (12.5).
+// topk 6 6.2 us (a whole warp: 9.4), 128 experts, topk 8 with a bias 9.4 us (12.5). Beyond, a
+// lane's 16 experts make the lists long: 256 experts in 8 groups 23.7 us (16.5).
 template <typename T>
 static cudaError_t launch_gate(GateArgs& p, cudaStream_t st) {
   if (p.n_group == 1) p.gsize = p.E;
