@@ -20,7 +20,7 @@ __device__ __forceinline__ bool mbar_test_wait_addr(uint32_t bar, uint32_t parit
 }
 
 // cluster_sync without its release: for threads that have published nothing,
-// or have fenced what they did.
+// have fenced what they did, or whose arrivals the other CTA has waited for.
 __device__ __forceinline__ void cluster_sync_relaxed() {
   asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }

@@ -236,6 +236,67 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(cfg):
     assert dg.get_device_error() == 0
 
 
+@pytest.mark.parametrize("cfg", [(128, 2, 1), (256, 2, 1)])
+def test_pairs_whose_second_cta_has_no_rows(cfg):
+    """The second CTA of a pair hands its accumulators back and is done before the
+    first: from one to five tiles a pair (both accumulators used never, once and
+    again), one K block and more than the ring holds, in runs of dependent launches."""
+    rng = np.random.default_rng(12)
+    dg.set_config(*cfg)
+    prev = dg.set_num_sms(2)
+    try:
+        for tiles in range(1, 6):
+            for K in (16, 128, 1040, 2064):
+                M, N = 100, cfg[0] * tiles - 16
+                (a, sa), (b, sb) = _codes(rng, M, K), _codes(rng, N, K)
+                t = _cuda(a, sa, b, sb)
+                d = [dg.int8_gemm_nt(*t) for _ in range(20)]
+                _check(d[0], routing.int8_gemm(a, sa, b, sb))
+                assert all(torch.equal(x, d[0]) for x in d)
+                # masked: pairs with rows of the first CTA only, of both, of none
+                counts, G = [128, 256, 0, 1, 129], 5
+                (a, sa), (b, sb) = _codes(rng, G, 256, K), _codes(rng, G, N, K)
+                t = _cuda(a, sa, b, sb, np.array(counts, np.int32))
+                d = [torch.full((G, 256, N), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(5)]
+                for x in d:
+                    dg.m_grouped_int8_gemm_nt_masked(*t, d=x)
+                for g, n in enumerate(counts):
+                    if n:
+                        _check(d[0][g, :n], routing.int8_gemm(a[g, :n], sa[g, :n], b[g], sb[g]))
+                    assert (d[0][g, n:] == 7).all()
+                assert all(torch.equal(x, d[0]) for x in d)
+        # contiguous: runs of one and of three blocks, each ending in a half-empty pair
+        a, sa, b, sb, idx = _contiguous(rng, [100, 300, 128], 272, 400)
+        t = _cuda(a, sa, b, sb, idx)
+        before = torch.full((len(idx), 272), 7.0, dtype=torch.bfloat16, device="cuda")
+        d = [before.clone() for _ in range(20)]
+        for x in d:
+            dg.m_grouped_int8_gemm_nt_contiguous(*t, d=x)
+        _check_contiguous(d[0], before, a, sa, b, sb, idx)
+        assert all(torch.equal(x, d[0]) for x in d)
+    finally:
+        dg.set_num_sms(prev)
+    assert dg.get_device_error() == 0
+
+
+@pytest.mark.parametrize("cfg", [(128, 2, 1), (256, 2, 1)])
+def test_a_pair_whose_wait_runs_out_is_reported_and_the_next_call_is_right(cfg):
+    rng = np.random.default_rng(14)
+    M, N, K = 256, 512, 32768
+    (a, sa), (b, sb) = _codes(rng, M, K), _codes(rng, N, K)
+    t = _cuda(a, sa, b, sb)
+    dg.set_config(*cfg)
+    prev = dg.set_wait_limit_ns(0)
+    try:
+        dg.int8_gemm_nt(*t)
+        torch.cuda.synchronize()
+    finally:
+        dg.set_wait_limit_ns(prev)
+    assert dg.get_device_error() & dg.DG_DEVERR_TIMEOUT
+    _check(dg.int8_gemm_nt(*t), routing.int8_gemm(a, sa, b, sb))
+    assert dg.get_device_error() == 0
+
+
 # ------------------------------------------------------------------ quantisation
 
 
