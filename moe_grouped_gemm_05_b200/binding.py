@@ -146,6 +146,17 @@ def _packed_numel(t, batch: int, mn: int, kb: int, name: str):
                          f"(batch x ceil(Kb/4) x align4(MN))")
 
 
+_INT_MAX = 0x7FFFFFFF
+
+
+def _c_ints(*sizes):
+    """Refuses sizes that are no C ints: ctypes would take them modulo 2^32.
+
+    Called where one of them is negative or beyond 31 bits, which the callers see by themselves in 0.1 us."""
+    if max(sizes) > _INT_MAX or min(sizes) < -_INT_MAX - 1:
+        raise ValueError(f"sizes {', '.join(str(n) for n in sizes)}: beyond 32 bits")
+
+
 def _same_device(ref, *tensors):
     """All operands of a call live on one device (None entries are skipped)."""
     dev = ref.get_device()
@@ -170,6 +181,8 @@ def pack_sf_ue8m0(sf: torch.Tensor, out=None) -> torch.Tensor:
     if s3.dim() != 3:
         raise ValueError("sf must be [mn, kb] or [batch, mn, kb]")
     batch, mn, kb = s3.shape
+    if (batch | mn | kb) >> 31:
+        _c_ints(batch, mn, kb)
     kp, mn4 = packed_sf_words(mn, kb)
     if out is None:
         out = torch.empty((batch, kp, mn4), dtype=torch.int32, device=sf.device)
@@ -196,6 +209,8 @@ def quantize_fp8_1x128(x: torch.Tensor, q=None, sf=None):
     batch = 1
     for n in lead:
         batch *= n
+    if (batch | M | K) >> 31:
+        _c_ints(batch, M, K)
     kp, mn4 = packed_sf_words(M, K // 128)
     if q is None:
         q = torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device)
@@ -227,6 +242,8 @@ def fp8_gemm_nt(a, sfa, b, sfb, d=None) -> torch.Tensor:
     _fp8(a, "a"), _fp8(b, "b"), _i32(sfb, "sfb")
     M, K = a.shape
     N, Kb_ = b.shape
+    if (M | N | K) >> 31:
+        _c_ints(M, N, K)
     if Kb_ != K:
         raise ValueError("a and b disagree on K")
     fp32_sfa = _sfa_kind(sfa, (M,), K)
@@ -256,6 +273,8 @@ def fp8_gemm(layout: str, a, sfa, b, sfb, d=None) -> torch.Tensor:
         raise ValueError("a and b must be contiguous")
     K, M = a.shape if layout[0] == "t" else a.shape[::-1]
     K2, N = b.shape if layout[1] == "n" else b.shape[::-1]
+    if (M | N | K) >> 31:
+        _c_ints(M, N, K)
     if K2 != K:
         raise ValueError("a and b disagree on K")
     if tuple(sfa.shape) != packed_sf_words(M, K // 128) or tuple(sfb.shape) != packed_sf_words(-(-N // 128), K // 128):
@@ -278,6 +297,8 @@ def fp8_gemm_nt_ex(a, sfa, b, sfb, c=None, d=None, recipe_b: int = 128, out_dtyp
     _fp8(a, "a"), _fp8(b, "b"), _i32(sfa, "sfa"), _i32(sfb, "sfb")
     M, K = a.shape
     N, Kb_ = b.shape
+    if (M | N | K | recipe_b) >> 31:
+        _c_ints(M, N, K, recipe_b)
     if Kb_ != K:
         raise ValueError("a and b disagree on K")
     if tuple(sfb.shape) != packed_sf_words(-(-N // recipe_b), K // 128) or tuple(sfa.shape) != packed_sf_words(M, K // 128):
@@ -303,6 +324,8 @@ def m_grouped_fp8_gemm_nt_contiguous(a, sfa, b, sfb, m_indices, d=None) -> torch
     _fp8(a, "a"), _fp8(b, "b"), _i32(sfb, "sfb"), _i32(m_indices, "m_indices")
     M, K = a.shape
     G, N, Kb_ = b.shape
+    if (M | N | K | G) >> 31:
+        _c_ints(M, N, K, G)
     if Kb_ != K or m_indices.shape != (M,):
         raise ValueError("shape mismatch")
     fp32_sfa = _sfa_kind(sfa, (M,), K)
@@ -326,6 +349,8 @@ def m_grouped_fp8_gemm_nt_masked(a, sfa, b, sfb, masked_m, d=None) -> torch.Tens
     _fp8(a, "a"), _fp8(b, "b"), _i32(sfb, "sfb"), _i32(masked_m, "masked_m")
     G, M_max, K = a.shape
     Gb, N, Kb_ = b.shape
+    if (G | M_max | N | K) >> 31:
+        _c_ints(G, M_max, N, K)
     if Gb != G or Kb_ != K or masked_m.shape != (G,):
         raise ValueError("shape mismatch")
     fp32_sfa = _sfa_kind(sfa, (G, M_max), K)
@@ -354,6 +379,8 @@ def moe_permute(topk_ids: torch.Tensor, num_experts: int, q: torch.Tensor, sfa: 
     if q.dim() != 2 or q.shape[0] != T:
         raise ValueError(f"q must be [T, K] with T = {T} rows, one per token of topk_ids")
     K = q.shape[1]
+    if (T | topk | num_experts | K) >> 31:
+        _c_ints(T, topk, num_experts, K)
     _packed_numel(sfa, 1, T, K // 128, "sfa")
     _same_device(q, topk_ids, sfa)
     cap = load().dg_moe_permute_capacity(T, topk, num_experts)
@@ -390,6 +417,8 @@ def moe_unpermute_combine(d_perm: torch.Tensor, row_of: torch.Tensor, weights=No
     _i32(row_of, "row_of")
     T, topk = row_of.shape
     N = d_perm.shape[1]
+    if (T | topk | N) >> 31:
+        _c_ints(T, topk, N)
     if weights is not None:
         _out(weights, (torch.float32,), (T, topk), "weights", d_perm.device)
     _same_device(d_perm, row_of)
@@ -426,7 +455,6 @@ def _operand(t, dtypes, shape, name: str, dev: int) -> int:
     return t.data_ptr()
 
 
-_INT_MAX = 0x7FFFFFFF
 _FLOAT_CODES = {torch.bfloat16: 0, torch.float32: 1}
 _INT8, _I32T, _F32T, _BF16T = (torch.int8,), (torch.int32,), (torch.float32,), (torch.bfloat16,)
 _BF16_F32 = (torch.bfloat16, torch.float32)
@@ -455,8 +483,8 @@ def moe_gate(logits, topk: int, bias=None, *, score: str = "softmax", n_group: i
     if score not in _SCORES:
         raise ValueError(f"unknown score {score!r}: softmax or sigmoid")
     (T, E), dev = _cuda_matrix(logits, _BF16_F32, "logits")
-    if max(T, n_group, topk_group, group_top) > _INT_MAX:     # ctypes would take them modulo 2^32
-        raise ValueError(f"{T} tokens, n_group={n_group}, topk_group={topk_group}, group_top={group_top}: beyond 32 bits")
+    if (T | E | topk | n_group | topk_group | group_top) >> 31:
+        _c_ints(T, E, topk, n_group, topk_group, group_top)
     if ids is None:
         ids = torch.empty((T, max(0, topk)), dtype=torch.int32, device=logits.device)
     if weights is None:
@@ -479,9 +507,9 @@ def moe_gate_backward(logits, topk_ids, d_weights, *, score: str = "softmax", re
     if score not in _SCORES:
         raise ValueError(f"unknown score {score!r}: softmax or sigmoid")
     (T, E), dev = _cuda_matrix(logits, _BF16_F32, "logits")
-    if T > _INT_MAX:
-        raise ValueError(f"{T} tokens: beyond 32 bits")
     topk = topk_ids.shape[-1] if topk_ids.dim() else 0
+    if (T | E | topk) >> 31:
+        _c_ints(T, E, topk)
     if d_logits is None:
         d_logits = torch.empty_like(logits)
     _check(load().dg_moe_gate_backward(logits.data_ptr(), _FLOAT_CODES[logits.dtype],
@@ -500,12 +528,15 @@ def quantize_int8_per_token(x, q=None, scale=None):
     """
     shape, dev = _cuda_matrix(x, _BF16_F32, "x", max(1, x.dim()))
     lead, K = shape[:-1], shape[-1]
+    M = lead.numel()
+    if (M | K) >> 31:
+        _c_ints(M, K)
     if q is None:
         q = torch.empty(shape, dtype=torch.int8, device=x.device)
     if scale is None:
         scale = torch.empty(lead, dtype=torch.float32, device=x.device)
     qp, sp = _operand(q, _INT8, shape, "q", dev), _operand(scale, _F32T, lead, "scale", dev)
-    _check(load().dg_quantize_int8_per_token(x.data_ptr(), _FLOAT_CODES[x.dtype], qp, sp, lead.numel(), K,
+    _check(load().dg_quantize_int8_per_token(x.data_ptr(), _FLOAT_CODES[x.dtype], qp, sp, M, K,
                                              _launch_stream(dev)))
     return q, scale
 
@@ -522,6 +553,8 @@ def moe_quantize_permute_int8(topk_ids, num_experts: int, x, out=None):
     if len(routed) != 2 or routed[0] != T:
         raise ValueError(f"topk_ids must be [T, topk] with T = {T} rows, one per token of x")
     topk = routed[1]
+    if (T | K | topk | num_experts) >> 31:
+        _c_ints(T, K, topk, num_experts)
     lib = load()
     cap = (T * topk + 127 * num_experts + 127) // 128 * 128    # dg_moe_permute_capacity
     if topk <= 0 or num_experts <= 0 or cap > _INT_MAX:
@@ -556,6 +589,8 @@ def int8_gemm_nt(a, sa, b, sb, d=None, out_dtype=torch.bfloat16) -> torch.Tensor
     """
     (M, K), dev = _cuda_matrix(a, _INT8, "a")
     N = b.shape[0]
+    if (M | N | K) >> 31:
+        _c_ints(M, N, K)
     if d is None:
         if out_dtype not in _BF16_F32:
             raise ValueError("out_dtype must be bfloat16 or float32")
@@ -572,6 +607,8 @@ def m_grouped_int8_gemm_nt_contiguous(a, sa, b, sb, m_indices, d=None) -> torch.
     untouched.  a int8 [M_total, K], sa float32 [M_total], b int8 [G, N, K], sb float32 [G, N], D bf16."""
     (M, K), dev = _cuda_matrix(a, _INT8, "a")
     (G, N, _), _ = _cuda_matrix(b, _INT8, "b", 3)
+    if (M | N | K | G) >> 31:
+        _c_ints(M, N, K, G)
     if d is None:
         d = torch.empty((M, N), dtype=torch.bfloat16, device=a.device)
     _check(load().dg_m_grouped_int8_gemm_nt_contiguous(
@@ -587,6 +624,8 @@ def m_grouped_int8_gemm_nt_masked(a, sa, b, sb, masked_m, d=None) -> torch.Tenso
     a int8 [G, M_max, K], sa float32 [G, M_max], b int8 [G, N, K], sb float32 [G, N], D bf16 [G, M_max, N]."""
     (G, M_max, K), dev = _cuda_matrix(a, _INT8, "a", 3)
     (_, N, _), _ = _cuda_matrix(b, _INT8, "b", 3)
+    if (G | M_max | N | K) >> 31:
+        _c_ints(G, M_max, N, K)
     if d is None:
         d = torch.empty((G, M_max, N), dtype=torch.bfloat16, device=a.device)
     _check(load().dg_m_grouped_int8_gemm_nt_masked(
@@ -611,11 +650,13 @@ def set_wait_limit_ns(ns: int) -> int:
 
 
 def set_num_sms(n: int) -> int:
+    _c_ints(n)
     return load().dg_set_num_sms(n)
 
 
 def set_tc_util(percent: int) -> int:
     """Caps the share of the GPU's SMs (tensor cores) a call may occupy; returns the previous percent."""
+    _c_ints(percent)
     prev = load().dg_set_tc_util(percent)
     if prev < 0:
         _check(prev)
@@ -629,12 +670,16 @@ def set_pdl(enable: bool) -> bool:
 
 def set_config(block_n: int, ctas: int = 0, pipes: int = 0) -> None:
     """Forces the N tile width, 1- or 2-CTA tiles and 1 or 2 pipelines per CTA (block_n=0: heuristic)."""
+    if (block_n | ctas | pipes) >> 31:
+        _c_ints(block_n, ctas, pipes)
     _check(load().dg_set_config(block_n, ctas, pipes))
 
 
 def describe_config(kind: str, M: int, N: int, K: int, num_groups: int = 1) -> str:
     buf = ctypes.create_string_buffer(64)
     k = {"dense": 0, "contiguous": 1, "masked": 2, "int8_dense": 3, "int8_contiguous": 4, "int8_masked": 5}[kind]
+    if (M | N | K | num_groups) >> 31:
+        _c_ints(M, N, K, num_groups)
     _check(load().dg_describe_config(k, M, N, K, num_groups, buf, 64))
     return buf.value.decode()
 

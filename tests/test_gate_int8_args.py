@@ -136,6 +136,82 @@ def test_sizes_beyond_32_bits_are_refused(monkeypatch):
             dg.moe_gate(torch.zeros(4, 16), 2, **{name: 2 ** 32 + 1})
 
 
+BIG = 2 ** 32 + 16        # 16 modulo 2^32, which every entry point takes
+
+
+def _meta(*shape, t=torch.int8):
+    return torch.empty(shape, dtype=t, device="meta")
+
+
+def _beyond():
+    """(name, call) for every size that the wrappers of the routing and int8 entry points pass on."""
+    f32, i32 = torch.float32, torch.int32
+    yield "gate E", lambda: dg.moe_gate(_meta(1, BIG, t=f32), 2)
+    yield "gate topk", lambda: dg.moe_gate(_meta(4, 16, t=f32), 2 ** 32 + 2)
+    yield "gate topk below", lambda: dg.moe_gate(_meta(4, 16, t=f32), -2 ** 32 + 2)
+    yield "gate n_group below", lambda: dg.moe_gate(_meta(4, 16, t=f32), 2, n_group=-2 ** 32 + 1)
+    yield "gradient E", lambda: dg.moe_gate_backward(_meta(1, BIG, t=f32), _meta(1, 2, t=i32), _meta(1, 2, t=f32))
+    yield "gradient topk", lambda: dg.moe_gate_backward(_meta(1, 16, t=f32), _meta(1, 2 ** 32 + 2, t=i32),
+                                                        _meta(1, 2 ** 32 + 2, t=f32))
+    yield "quantize K", lambda: dg.quantize_int8_per_token(_meta(1, BIG, t=f32))
+    yield "quantize M", lambda: dg.quantize_int8_per_token(_meta(2 ** 16, 2 ** 16 + 1, 16, t=f32))
+    yield "permute T", lambda: dg.moe_quantize_permute_int8(_meta(BIG, 2, t=i32), 4, _meta(BIG, 16, t=f32))
+    yield "permute K", lambda: dg.moe_quantize_permute_int8(_meta(4, 2, t=i32), 4, _meta(4, BIG, t=f32))
+    yield "permute topk", lambda: dg.moe_quantize_permute_int8(_meta(4, BIG, t=i32), 4, _meta(4, 16, t=f32))
+    yield "permute experts", lambda: dg.moe_quantize_permute_int8(_meta(4, 2, t=i32), 2 ** 32 + 4, _meta(4, 16, t=f32))
+    for name, (M, N, K) in (("M", (BIG, 16, 16)), ("N", (16, BIG, 16)), ("K", (16, 16, BIG))):
+        a, b, sa, sb = _meta(M, K), _meta(N, K), _meta(M, t=f32), _meta(N, t=f32)
+        yield f"dense {name}", lambda a=a, b=b, sa=sa, sb=sb: dg.int8_gemm_nt(a, sa, b, sb)
+        yield f"contiguous {name}", lambda a=a, b=b, sa=sa, sb=sb: dg.m_grouped_int8_gemm_nt_contiguous(
+            a, sa, b[None], sb[None], _meta(a.shape[0], t=i32))
+        yield f"masked {name}", lambda a=a, b=b, sa=sa, sb=sb: dg.m_grouped_int8_gemm_nt_masked(
+            a[None], sa[None], b[None], sb[None], _meta(1, t=i32))
+    yield "contiguous G", lambda: dg.m_grouped_int8_gemm_nt_contiguous(
+        _meta(128, 16), _meta(128, t=f32), _meta(BIG, 16, 16), _meta(BIG, 16, t=f32), _meta(128, t=i32))
+    yield "masked G", lambda: dg.m_grouped_int8_gemm_nt_masked(
+        _meta(BIG, 1, 16), _meta(BIG, 1, t=f32), _meta(BIG, 16, 16), _meta(BIG, 16, t=f32), _meta(BIG, t=i32))
+
+
+@pytest.mark.parametrize("name,call", [pytest.param(n, c, id=n) for n, c in _beyond()])
+def test_no_size_is_taken_modulo_2_to_the_32(name, call, monkeypatch):
+    """A size of 2^32 + 16 must not reach the library, which would see 16."""
+    reached = []
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *args: reached.append((name, args)) or 0
+
+    monkeypatch.setattr(dg, "_cuda_matrix", lambda t, *args: (t.shape, 0))
+    monkeypatch.setattr(dg, "_operand", lambda t, *args: 0x10000)
+    monkeypatch.setattr(dg, "_launch_stream", lambda dev: 0)
+    monkeypatch.setattr(dg, "load", lambda: Library())
+    with pytest.raises(ValueError, match="32 bits"):
+        call()
+    assert not reached
+
+
+def test_fp8_sizes_beyond_32_bits_are_refused(monkeypatch):
+    for name in ("_fp8", "_i32", "_sfa_kind", "_packed_numel"):
+        monkeypatch.setattr(dg, name, lambda *args: False)
+    i32 = torch.int32
+    for M, N, K in ((BIG, 16, 128), (16, BIG, 128), (16, 16, 2 ** 32 + 128)):
+        a, b, s = _meta(M, K), _meta(N, K), _meta(1, 4, t=i32)
+        for call in (lambda: dg.fp8_gemm_nt(a, s, b, s), lambda: dg.fp8_gemm_nt_ex(a, s, b, s),
+                     lambda: dg.fp8_gemm("nn", a, s, _meta(K, N), s),
+                     lambda: dg.m_grouped_fp8_gemm_nt_contiguous(a, s, b[None], s, _meta(M, t=i32)),
+                     lambda: dg.m_grouped_fp8_gemm_nt_masked(a[None], s, b[None], s, _meta(1, t=i32))):
+            with pytest.raises(ValueError, match="32 bits"):
+                call()
+    with pytest.raises(ValueError, match="32 bits"):
+        dg.moe_permute(_meta(4, 2, t=i32), 2 ** 32 + 4, _meta(4, 128), s)
+    with pytest.raises(ValueError, match="32 bits"):
+        dg.describe_config("dense", 2 ** 32 + 64, 256, 256)
+    for call in (lambda: dg.set_num_sms(2 ** 32 + 8), lambda: dg.set_tc_util(2 ** 32 + 50),
+                 lambda: dg.set_config(2 ** 32 + 128)):
+        with pytest.raises(ValueError, match="32 bits"):
+            call()
+
+
 def test_operands_of_another_device_than_the_current_one_are_refused(monkeypatch):
     monkeypatch.setattr(dg, "_current_device", lambda: 1)
     monkeypatch.setattr(dg, "_current_stream", lambda dev: 7 + dev)
