@@ -428,6 +428,9 @@ static const Config* choose_config(long long rows_est, int N, int K, int sms, in
   return best;
 }
 
+// Blocks of `block` that cover n (no sum that could leave int for n next to 2^31).
+static int blocks_of(int n, int block) { return n / block + (n % block != 0); }
+
 static int raster_group(int num_m_blocks) { return std::min(num_m_blocks, 16); }
 
 // Clusters of two CTAs must sit in one GPC, so fewer than sms/2 pairs may be
@@ -709,7 +712,7 @@ static const Config* choose_int8_config(long long rows_est, int N, int K, int sm
       // a run of blocks of odd length, every other expert's, ends in a half-empty pair
       if (mode == MODE_CONTIG && c.ctas == 2) m_tiles += (groups + 3) / 4;
     }
-    const long long n_tiles = (N + c.bn - 1) / c.bn;
+    const long long n_tiles = blocks_of(N, c.bn);
     const long long units = std::max(1, sms / c.ctas);
     const double waves = static_cast<double>((m_tiles * n_tiles + units - 1) / units);
     const double compute = waves * (((K + 127) / 128) * (c.splitk ? 0.5 : 1.0) * k.kb_ns + k.tile_ns);
@@ -768,8 +771,8 @@ static int int8_gemm(const void* a, const float* sa, const void* b, const float*
   args.N = N;
   args.K = K;
   args.G = GB;
-  args.num_m_blocks = (rows + 128 * cfg->ctas - 1) / (128 * cfg->ctas);
-  args.num_n_blocks = (N + cfg->bn - 1) / cfg->bn;
+  args.num_m_blocks = blocks_of(rows, 128 * cfg->ctas);
+  args.num_n_blocks = blocks_of(N, cfg->bn);
   args.raster_m = raster_group(args.num_m_blocks);
   args.m_indices = m_indices;
   args.masked_m = masked_m;
@@ -1071,15 +1074,15 @@ int dg_describe_config(int kind, int M, int N, int K, int num_groups, char* buf,
         : kind == 4 ? choose_int8_config<MODE_CONTIG>(est, N, K, sms, num_groups)
                     : choose_int8_config<MODE_MASKED>(est, N, K, sms, num_groups);
     if (c)
-      tiles = static_cast<long long>(kind == 5 ? num_groups : 1) * ((M + 128 * c->ctas - 1) / (128 * c->ctas)) *
-              ((N + c->bn - 1) / c->bn);
+      tiles = static_cast<long long>(kind == 5 ? num_groups : 1) * blocks_of(M, 128 * c->ctas) *
+              blocks_of(N, c->bn);
   } else if (kind == 2) {
     const long long est = std::max<long long>(1, static_cast<long long>(num_groups) * M / 2);
     c = choose_config<MODE_MASKED>(est, N, K, sms, num_groups, M);
-    if (c) tiles = static_cast<long long>(num_groups) * ((M + 128 * c->ctas - 1) / (128 * c->ctas)) * ((N + c->bn - 1) / c->bn);
+    if (c) tiles = static_cast<long long>(num_groups) * blocks_of(M, 128 * c->ctas) * blocks_of(N, c->bn);
   } else {
     c = kind == 1 ? choose_config<MODE_CONTIG>(M, N, K, sms, num_groups) : choose_config<MODE_DENSE>(M, N, K, sms);
-    if (c) tiles = static_cast<long long>((M + 128 * c->ctas - 1) / (128 * c->ctas)) * ((N + c->bn - 1) / c->bn);
+    if (c) tiles = static_cast<long long>(blocks_of(M, 128 * c->ctas)) * blocks_of(N, c->bn);
   }
   if (!c) return fail(DG_ERR_UNSUPPORTED, "no configuration");
   snprintf(buf, buflen, "%dx%dx%d%s%s%s%s/%d", 128 * c->ctas, c->bn, c->stages, c->ctas == 2 ? "(2cta)" : "",

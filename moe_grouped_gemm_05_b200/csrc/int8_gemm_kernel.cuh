@@ -94,7 +94,7 @@ __device__ __forceinline__ void masked_tile_prefix(const GemmArgs& p, int* prefi
         mg = mg < 0 ? 0 : p.rows;
       }
       counts[g] = mg;
-      tiles = ((mg + TILE_M - 1) / TILE_M) * p.num_n_blocks;
+      tiles = static_cast<int>((static_cast<uint32_t>(mg) + TILE_M - 1) / TILE_M) * p.num_n_blocks;
     }
     int incl = tiles;
 #pragma unroll
@@ -477,7 +477,7 @@ __global__ void __launch_bounds__(kInt8Threads<PIPES>, 1)
           if (PIPES == 2) mbar_arrive(&tmem_empty[1]);
         }
       };
-      const int mine = any_valid ? min(kMine, max(0, ((p.N - n0 + 31) / 32 - half + 1) / 2)) : 0;
+      const int mine = any_valid ? min(kMine, max(0, ((min(p.N - n0, BN) + 31) / 32 - half + 1) / 2)) : 0;
       if (mine == 0) {
         release();
         continue;

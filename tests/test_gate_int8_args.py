@@ -220,6 +220,25 @@ def test_operands_of_another_device_than_the_current_one_are_refused(monkeypatch
         dg._launch_stream(0)
 
 
+def test_tiles_are_counted_at_the_ends_of_int(lib):
+    """2^31 - 1 rows or 2^31 - 16 columns are millions of tiles: the grid must be as
+    full as for a million rows (a sum beyond int had left none of them)."""
+    most = 2 ** 31 - 1
+    for ctas in (1, 2):
+        assert lib.dg_set_config(128, ctas, 1) == 0
+        try:
+            for kind in ("int8_dense", "int8_contiguous", "int8_masked", "dense", "masked"):
+                want = dg.describe_config(kind, 2 ** 20, 16, 128, 1)
+                assert want.split("/")[1] == "148"
+                assert dg.describe_config(kind, most, 16, 128, 1) == dg.describe_config(kind, 2 ** 24, 16, 128, 1)
+                assert dg.describe_config(kind, 1, most - 15, 128, 1).split("/")[1] == "148"
+        finally:
+            assert lib.dg_set_config(0, 0, 0) == 0
+    for kind in ("int8_dense", "int8_contiguous", "int8_masked"):
+        assert dg.describe_config(kind, most, 7168, 2048, 4).split("/")[1] == "148"
+        assert dg.describe_config(kind, 64, most - 15, 2048, 4).split("/")[1] == "148"
+
+
 def test_int8_tile_choice(lib):
     """The heuristic is host logic (148 SMs assumed without a device): narrow
     1-CTA tiles for a few rows, pairs of CTAs for many, no pairs beyond the

@@ -297,6 +297,53 @@ def test_a_pair_whose_wait_runs_out_is_reported_and_the_next_call_is_right(cfg):
     assert dg.get_device_error() == 0
 
 
+@pytest.mark.parametrize("cfg", [None, (128, 2, 1)])
+def test_row_and_column_counts_next_to_2_to_the_31(cfg):
+    """The largest row counts of every layout and the largest column count, every element:
+    sums of 16 products are exact in FP32, so torch's product takes the same roundings."""
+    most, K = 2 ** 31 - 1, 16
+    torch.cuda.empty_cache()
+    if torch.cuda.mem_get_info()[0] < 140 << 30:
+        pytest.skip("140 GiB of device memory needed")
+    g = torch.Generator(device="cuda").manual_seed(1)
+    a = torch.empty((most, K), dtype=torch.int8, device="cuda").random_(-128, 128, generator=g)
+    sa = torch.empty(most, device="cuda").uniform_(0.5, 1.5, generator=g)
+    b, sb = a[:K].clone(), sa[:K].clone()
+    d = torch.empty((most, K), dtype=torch.bfloat16, device="cuda")
+
+    def check(rows):
+        for i in range(0, most, 2 ** 25):
+            p = slice(i, min(most, i + 2 ** 25))
+            want = ((a[p].float() @ b.float().t()) * sa[p, None] * sb).to(torch.bfloat16)
+            if p.stop > rows:
+                want[max(0, rows - i):] = 7
+            assert torch.equal(d[p], want), i
+        d.fill_(7)
+
+    if cfg:
+        dg.set_config(*cfg)
+    d.fill_(7)
+    dg.int8_gemm_nt(a, sa, b, sb, d=d)
+    check(most)
+    counts = torch.tensor([most], dtype=torch.int32, device="cuda")
+    dg.m_grouped_int8_gemm_nt_masked(a[None], sa[None], b[None], sb[None], counts, d=d[None])
+    check(most)
+    whole = most // 128 * 128
+    idx = torch.zeros(whole, dtype=torch.int32, device="cuda")
+    dg.m_grouped_int8_gemm_nt_contiguous(a[:whole], sa[:whole], b[None], sb[None], idx, d=d[:whole])
+    check(whole)
+    del idx, d
+    # one row against 2^31 - 16 columns
+    N = most - 15
+    d = dg.int8_gemm_nt(b[:1], sb[:1], a[:N], sa[:N])
+    for i in range(0, N, 2 ** 25):
+        p = slice(i, min(N, i + 2 ** 25))
+        assert torch.equal(d[:, p], ((b[:1].float() @ a[p].float().t()) * sb[:1, None] * sa[p]).to(torch.bfloat16)), i
+    assert dg.get_device_error() == 0
+    del a, sa, d
+    torch.cuda.empty_cache()
+
+
 # ------------------------------------------------------------------ quantisation
 
 
