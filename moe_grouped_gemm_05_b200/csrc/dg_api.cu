@@ -401,11 +401,15 @@ template <int MODE>
 static const Config* choose_config(long long rows_est, int N, int K, int sms, int groups = 1,
                                    long long a_extent = -1) {
   if (a_extent < 0) a_extent = rows_est;
+  // a CTA pair needs two SMs; contiguous pairs fit the device-built pair table of kMaxContigBlocks blocks
+  const auto pairs_fit = [&](const Config& c) {
+    return c.ctas <= sms && !(MODE == MODE_CONTIG && c.ctas == 2 && rows_est / 128 > kMaxContigBlocks);
+  };
   // A forced tile applies to the entry points that have it built; the others
   // keep the heuristic (each layout and output type builds its own set).
   if (t_force_bn) {
     const Config* f = find_config<MODE>(t_force_bn, t_force_ctas, t_force_pipes, a_extent);
-    if (f && !(MODE == MODE_CONTIG && f->ctas == 2 && rows_est / 128 > kMaxContigBlocks)) return f;
+    if (f && pairs_fit(*f)) return f;
   }
   int n = 0;
   const Config* t = config_table<MODE>(&n);
@@ -416,8 +420,7 @@ static const Config* choose_config(long long rows_est, int N, int K, int sms, in
     if (!a_rows_fit(c, a_extent)) continue;
     // split-K tiles keep no second accumulator for overlap; they need at least two groups of 4 K blocks
     if (c.splitk && K <= 4 * 128) continue;
-    // contiguous CTA pairs: the device-built pair table holds kMaxContigBlocks blocks
-    if (MODE == MODE_CONTIG && c.ctas == 2 && rows_est / 128 > kMaxContigBlocks) continue;
+    if (!pairs_fit(c)) continue;
     const double cost = config_cost<MODE == MODE_CONTIG || MODE == MODE_MASKED ? MODE : MODE_DENSE>(
         c, rows_est, N, K, sms, groups);
     if (cost < best_cost * 0.999) {
@@ -687,9 +690,9 @@ static const Config* choose_int8_config(long long rows_est, int N, int K, int sm
   constexpr int mode = MODE == MODE_INT8_DENSE_F32 ? MODE_DENSE : MODE;
   int n = 0;
   const Config* t = int8_config_table<MODE>(&n);
-  // pairs within the contiguous layout's table; a K block at least for each of two pipelines
+  // two SMs a pair; pairs within the contiguous layout's table; a K block at least for each of two pipelines
   const auto fits = [&](const Config& c) {
-    return !(mode == MODE_CONTIG && c.ctas == 2 && rows_est / 128 > kMaxContigBlocks) && !(c.pipes == 2 && K <= 128);
+    return c.ctas <= sms && !(mode == MODE_CONTIG && c.ctas == 2 && rows_est / 128 > kMaxContigBlocks) && !(c.pipes == 2 && K <= 128);
   };
   if (t_force_bn)
     for (int i = 0; i < n; ++i)

@@ -239,6 +239,24 @@ def test_tiles_are_counted_at_the_ends_of_int(lib):
         assert dg.describe_config(kind, 64, most - 15, 2048, 4).split("/")[1] == "148"
 
 
+@pytest.mark.parametrize("sms", [1, 2, 3])
+def test_few_sms_still_get_a_grid(lib, sms):
+    """A CTA pair needs two SMs: with one, neither the heuristic nor a forced tile
+    takes pairs (their grid would be empty), whatever the layout."""
+    kinds = ["dense", "contiguous", "masked", "int8_dense", "int8_contiguous", "int8_masked"]
+    prev = dg.set_num_sms(sms)
+    try:
+        for forced in [(0, 0, 0), (128, 2, 1), (256, 2, 1), (224, 2, 2), (256, 2, 0)]:
+            assert lib.dg_set_config(*forced) == 0
+            for kind in kinds:
+                for M, N, K in ((128, 256, 256), (4096, 7168, 2048), (32768, 4096, 7168)):
+                    tile, grid = dg.describe_config(kind, M, N, K, 8).split("/")
+                    assert 1 <= int(grid) <= sms and (sms > 1 or "(2cta)" not in tile), (kind, M, forced)
+    finally:
+        assert lib.dg_set_config(0, 0, 0) == 0
+        dg.set_num_sms(prev)
+
+
 def test_int8_tile_choice(lib):
     """The heuristic is host logic (148 SMs assumed without a device): narrow
     1-CTA tiles for a few rows, pairs of CTAs for many, no pairs beyond the

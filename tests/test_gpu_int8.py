@@ -15,7 +15,7 @@ from moe_grouped_gemm_05_b200 import binding as dg
 from moe_grouped_gemm_05_b200 import synth
 from oracle import routing
 
-from helpers import bits, check_close
+from helpers import bits, check_close, packed, to_device
 
 pytestmark = pytest.mark.gpu
 CONFIGS = [(64, 1, 1), (128, 1, 1), (256, 1, 1), (128, 2, 1), (256, 2, 1), (64, 1, 2), (128, 1, 2)]
@@ -233,6 +233,33 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right(cfg):
         dg.set_wait_limit_ns(prev)
     assert dg.get_device_error() & dg.DG_DEVERR_TIMEOUT
     _check(dg.int8_gemm_nt(*t), routing.int8_gemm(a, sa, b, sb))
+    assert dg.get_device_error() == 0
+
+
+def test_one_sm():
+    """Products that take CTA pairs on more SMs, on one (which holds no pair)."""
+    rng = np.random.default_rng(15)
+    (a, sa), (b, sb) = _codes(rng, 300, 272), _codes(rng, 528, 272)
+    idx = np.repeat(np.arange(3, dtype=np.int32), 128)
+    (x, sx), (w, sw) = _codes(rng, 384, 272), _codes(rng, 3, 528, 272)
+    want = dg.int8_gemm_nt(*_cuda(a, sa, b, sb))
+    grouped = dg.m_grouped_int8_gemm_nt_contiguous(*_cuda(x, sx, w, sw, idx))
+    t = _cuda(x.reshape(3, 128, 272), sx.reshape(3, 128), w, sw, np.full(3, 128, np.int32))
+    prev = dg.set_num_sms(1)
+    try:
+        for cfg in ((0, 0, 0), (256, 2, 1)):
+            dg.set_config(*cfg)
+            assert torch.equal(dg.int8_gemm_nt(*_cuda(a, sa, b, sb)), want)
+            assert torch.equal(dg.m_grouped_int8_gemm_nt_contiguous(*_cuda(x, sx, w, sw, idx)), grouped)
+            assert torch.equal(dg.m_grouped_int8_gemm_nt_masked(*t).reshape(384, 528), grouped)
+        p = synth.dense_problem(300, 528, 256, seed=3)
+        qa, qb = packed(p)
+        f = to_device(p, qa, qb)
+        d = dg.fp8_gemm_nt(f["a"], f["sfa"], f["b"], f["sfb"])
+        check_close(bits(d), oracle.fp8_gemm_nt(p.a, qa, p.b, qb, 300, 528, 256), "one SM")
+    finally:
+        dg.set_num_sms(prev)
+    _check(want, routing.int8_gemm(a, sa, b, sb))
     assert dg.get_device_error() == 0
 
 
