@@ -799,12 +799,10 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
   const float s = has ? gate_at(row, mine_id) : -INFINITY;  // the chosen expert's logit
   float w;
   if (p.renorm) {
-    // s_j / sum s; from the ratios to the largest, where the scores might underflow
+    // s_j / sum s, from e^(s - hi) or e^(min(s, 0) - min(hi, 0)) / (1 + e^-|s|): ratios to the
+    // largest, so no share that is itself a normal number underflows on the way
     const float hi = team_max<L>(s);
-    float v;
-    if (!SIGMOID) v = expf(s - hi);
-    else if (hi > -60.0f) v = __fdiv_rn(1.0f, 1.0f + expf(-s));
-    else v = __fdiv_rn(expf(s - hi), 1.0f + expf(s));
+    float v = SIGMOID ? __fdiv_rn(expf(fminf(s, 0.0f) - fminf(hi, 0.0f)), 1.0f + expf(-fabsf(s))) : expf(s - hi);
     v = has ? v : 0.0f;
     w = __fdiv_rn(v, team_sum<L>(v));
   } else if (SIGMOID) {

@@ -235,6 +235,24 @@ def test_extreme_logits():
     check_gate(l, 8, torch.zeros(E), score="sigmoid")
 
 
+@pytest.mark.parametrize("best", [-0.5, -30.0, -59.0, -61.0, 0.0, 3.0])
+def test_sigmoid_shares_far_below_the_best(best):
+    """Chosen logits down to 85 (and, where the share is still a normal number, 120) below
+    the best: their shares are e^-36 and less, and not zero."""
+    rng = np.random.default_rng(int(best * 2) + 200)
+    T, E = 40, 24
+    l = torch.full((T, E), best)
+    l[:, 1:] = torch.from_numpy(best - rng.uniform(30, 84, (T, E - 1)))
+    l[::2, 1:8] = torch.from_numpy(rng.uniform(-120, -85, (T // 2, 7)))
+    for topk in (2, 8, 24):
+        for scale in (1.0, 2.5):
+            _, w = check_gate(l, topk, score="sigmoid", renormalize=True, scale=scale)
+            assert (w[1::2] > 0).all()
+    l = torch.tensor([[-59.0, -95.0]])
+    _, w = check_gate(l, 2, score="sigmoid", renormalize=True)
+    assert 2.3e-16 < float(w[0, 1]) < 2.4e-16
+
+
 def test_outputs_beyond_the_rows_stay_and_no_tokens_is_nothing():
     ids = torch.full((12, 3), 77, dtype=torch.int32, device="cuda")
     w = torch.full((12, 3), 77.0, device="cuda")
