@@ -434,6 +434,16 @@ __device__ __forceinline__ float group_error(float e0, float a1, float a2, int g
   const float sum = fabsf(a1 + a2);
   return err + e0 + fminf(u * x2, 1.0f) + fminf(sum < INFINITY ? u * sum : INFINITY, fminf(x1, x2));
 }
+// No less than group_error but for a sum that was cut off at the type's range, in fewer
+// steps; with two units of `mine` for the roundings of mine + and - the margin.  (A cut off
+// sum is right where this is used: the true one of a group that is not kept is lower still,
+// at the top of the range groups are equal, and at its bottom none that is left out has a
+// score.)  Taken for each group by itself, so that one with experts pushed out by a bias of
+// any size brings no other into question.
+__device__ __forceinline__ float group_margin(float e0, float a1, float a2, float mine, int group_top) {
+  const float x2 = group_top == 1 || a2 == -INFINITY ? 0.0f : fabsf(a2);
+  return 2.0f * e0 + fminf(0x1.01p-24f * (fabsf(a1) + x2), 2.0f) + 0x1.81p-23f * fabsf(mine);
+}
 
 template <typename LT, int L, int V, bool SIGMOID, bool BIAS>
 __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_constant__ GateArgs p) {
@@ -560,17 +570,16 @@ __global__ void __launch_bounds__(32 * kGateWarps) moe_gate_kernel(const __grid_
     const float mine = group_score(a1, a2, p.group_top);
     // lanes behind the last group have -inf, as groups without an expert to choose
     const bool some = mine > -INFINITY;
-    // no less than twice the largest group_error, in fewer steps
-    const float gnear =
-        scored ? 4.0f * e0 + 0x1.01p-22f * team_max<L>(some ? fabsf(a1) + fabsf(a2) : 0.0f) : 0.0f;
-    // the topk_group-th best score, and the best below it
+    // the topk_group-th best score
     const float kth = team_kth<L>(mine, L == 32 ? p.topk_group : p.topk_group * span, lane);
     bool kept = some && mine >= kth;
-    const float below = team_max<L>(mine < kth ? mine : -INFINITY);
+    const float err = scored ? group_margin(e0, a1, a2, mine, p.group_top) : 0.0f;
+    // what the lowest kept score may be at least, and the highest of the others at most
+    const float least_kept = -team_max<L>(kept ? err - mine : -INFINITY);
+    const float most_other = team_max<L>(some && !kept ? mine + err : -INFINITY);
     // (every lane votes, whatever its team found: no vote behind a condition that teams may differ in)
     const int lanes_kept = __popc(team_ballot<L>(kept, lane));
-    const bool slow = (scored && kth - below <= gnear) ||  // (-inf - -inf is NaN: not close)
-                      lanes_kept > p.topk_group * span;
+    const bool slow = (most_other > -INFINITY && most_other >= least_kept) || lanes_kept > p.topk_group * span;
     if (__any_sync(0xffffffffu, slow)) {
       // a close call, or equal scores: rank the groups one by one
       const float gerr = scored && some ? group_error(e0, a1, a2, p.group_top) : 0.0f;

@@ -210,6 +210,28 @@ def test_biases_of_any_size(T, E, topk, n_group, topk_group, score):
     check_gate(l, topk, b, group_top=min(2, E // n_group), **kw)
 
 
+@pytest.mark.parametrize("value", [torch.finfo(torch.float32).min, -1e9, -300.0, 1e9, torch.finfo(torch.float32).max, -INF])
+@pytest.mark.parametrize("E,n_group,topk_group,topk", [(256, 8, 4, 8), (64, 8, 3, 6), (60, 6, 2, 4), (8, 8, 4, 2),
+                                                       (1020, 17, 5, 12)])
+def test_whole_groups_with_the_same_large_bias(E, n_group, topk_group, topk, value):
+    """Groups that a bias pushes out (or in) as a whole, all but for one expert, or with one
+    term of each sign: for a few groups, so that enough others are left, and for all but one."""
+    gsize = E // n_group
+    l = _rand(60, E, E + 5)
+    l[50:] = l[:1]                                       # (and rows next to one another in value)
+    l[52:, ::2] += 2.0 ** -20
+    for score in ("softmax", "sigmoid"):
+        for pushed in (1, n_group - topk_group, n_group - 1):
+            for keep in (0, 1, 2):
+                b = 0.05 * _rand(1, E, 9)[0]
+                for g in range(pushed):
+                    b[g * gsize + keep:(g + 1) * gsize] = value
+                    if keep == 2 and gsize > 2 and abs(value) < 1e30:
+                        b[g * gsize] = -value
+                for group_top in {1, min(2, gsize)}:
+                    check_gate(l, topk, b, score=score, n_group=n_group, topk_group=topk_group, group_top=group_top)
+
+
 @pytest.mark.parametrize("what", [float("nan"), INF])
 def test_rows_that_are_not_numbers_are_not_routed(what):
     l = _rand(10, 60, 41)
