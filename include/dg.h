@@ -247,7 +247,9 @@ int dg_moe_unpermute_combine(const void* d_perm, const int32_t* row_of, const fl
  * -1 and weight 0 (a padded token: every logit -infinity), which the permutations
  * and the combine take as not routed.  A row with a NaN or +infinity (or such a
  * bias) is not routed at all and sets DG_DEVERR_BAD_LOGIT.  At most 1024 experts,
- * 32 groups and topk 32; topk <= topk_group * num_experts / n_group.
+ * 32 groups and topk 32; topk <= topk_group * num_experts / n_group.  logits, d_logits
+ * and bias are aligned as the rows of a 16-byte aligned matrix are (to 16 bytes, or to
+ * the largest power of two that divides a row): a batch may start at any token.
  *
  * dg_moe_gate_backward: d_logits [T][num_experts], in the logits' type, from
  * d_weights FP32 [T][topk], the gradient of topk_weights, with the choice of

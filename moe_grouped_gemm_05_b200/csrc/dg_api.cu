@@ -1485,6 +1485,14 @@ int dg_moe_quantize_permute_int8(const int32_t* topk_ids, int T, int topk, int n
   return DG_OK;
 }
 
+// Alignment of a matrix with rows of row_bytes: 16, or the largest power of two that
+// divides a row, so that a matrix may start at any row of an aligned one.  (The kernels'
+// accesses of a row are no wider: they divide it.)
+static bool row_aligned(const void* p, size_t row_bytes) {
+  const size_t both = row_bytes | 16;
+  return (reinterpret_cast<uintptr_t>(p) & ((both & (~both + 1)) - 1)) == 0;  // its lowest bit set, less one
+}
+
 static int check_gate(const void* logits, int logits_dtype, const void* ids, const void* w, const void* d, int T, int E,
                       int topk, int score_func, int renormalize) {
   if (logits_dtype != 0 && logits_dtype != 1)
@@ -1498,7 +1506,9 @@ static int check_gate(const void* logits, int logits_dtype, const void* ids, con
     return fail(DG_ERR_SHAPE, "topk=%d must be in [1, min(%d, num_experts=%d)]", topk, kGateMaxTopk, E);
   if (T == 0) return DG_OK;
   if (!logits || !ids || !w || !d) return fail(DG_ERR_NULL, "every pointer but bias must be non-NULL");
-  if (!aligned16(logits) || !aligned16(d)) return fail(DG_ERR_ALIGN, "logits and d_logits must be 16-byte aligned");
+  const size_t row = static_cast<size_t>(E) * (logits_dtype == 0 ? 2 : 4);
+  if (!row_aligned(logits, row) || !row_aligned(d, row))
+    return fail(DG_ERR_ALIGN, "logits and d_logits must be aligned as the rows of a 16-byte aligned matrix");
   if ((reinterpret_cast<uintptr_t>(ids) & 3) != 0 || (reinterpret_cast<uintptr_t>(w) & 3) != 0)
     return fail(DG_ERR_ALIGN, "topk_ids and the weights must be 4-byte aligned");
   return DG_OK;
@@ -1509,7 +1519,8 @@ int dg_moe_gate(const void* logits, int logits_dtype, const float* bias, int T, 
                 int32_t* topk_ids, float* topk_weights, void* stream) {
   int r = check_gate(logits, logits_dtype, topk_ids, topk_weights, logits, T, num_experts, topk, score_func, renormalize);
   if (r) return r;
-  if (bias && !aligned16(bias)) return fail(DG_ERR_ALIGN, "bias must be 16-byte aligned");
+  if (bias && !row_aligned(bias, static_cast<size_t>(num_experts) * 4))
+    return fail(DG_ERR_ALIGN, "bias must be aligned as the rows of a 16-byte aligned matrix");
   if (n_group <= 0 || n_group > kGateMaxGroups || num_experts % n_group != 0)
     return fail(DG_ERR_SHAPE, "n_group=%d must divide num_experts=%d and be at most %d", n_group, num_experts,
                 kGateMaxGroups);

@@ -97,6 +97,22 @@ def test_gate_refusals(lib):
     assert backward(T=0, l=NULL, d=NULL) == 0
 
 
+def test_gate_alignment_goes_by_the_rows_length(lib):
+    """Rows of 120 bytes start at multiples of 8, rows of 66 at multiples of 2, rows of 256 at multiples of 16."""
+    def gate(l, E, t, bias=NULL):
+        return lib.dg_moe_gate(l, t, bias, 10, E, 2, 1, 1, 1, 1, 0, 1.0, GOOD, GOOD, None)
+
+    def backward(l, d, E, t):
+        return lib.dg_moe_gate_backward(l, t, GOOD, GOOD, 10, E, 2, 1, 0, 1.0, d, None)
+
+    odd4, odd1 = P(0x10004), P(0x10001)
+    for E, t, bad in ((64, 1, ODD8), (64, 0, ODD8), (60, 1, ODD8), (60, 0, odd4), (33, 1, ODD2), (33, 0, odd1),
+                      (34, 0, ODD2), (100, 0, odd4)):
+        assert gate(bad, E, t) == dg.DG_ERR_ALIGN, (E, t)
+        assert backward(bad, GOOD, E, t) == backward(GOOD, bad, E, t) == dg.DG_ERR_ALIGN, (E, t)
+    assert gate(GOOD, 64, 0, bias=ODD8) == gate(GOOD, 33, 0, bias=ODD2) == dg.DG_ERR_ALIGN
+
+
 def test_binding_refuses_before_the_library_is_called():
     x = torch.zeros(4, 16)
     with pytest.raises(ValueError, match="CUDA"):

@@ -275,6 +275,30 @@ def test_sigmoid_shares_far_below_the_best(best):
     assert 2.3e-16 < float(w[0, 1]) < 2.4e-16
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("E,n_group", [(60, 1), (60, 6), (33, 1), (66, 3), (100, 5), (34, 2), (260, 1), (1020, 17), (7, 1)])
+def test_a_batch_that_starts_at_any_row(E, n_group, dtype):
+    """Slices of a larger batch: rows of 120 bytes start at multiples of 8, rows of 66 at multiples of 2."""
+    T, topk = 21, 3
+    whole = _rand(T + 8, E, E, dtype).cuda()
+    d_whole = torch.full_like(whole, 7.0)
+    bias = torch.zeros(3, E, device="cuda")
+    bias[1] = 0.05 * _rand(1, E, 9)[0].cuda()
+    kw = dict(score="sigmoid", renormalize=True)
+    for first in (1, 2, 3, 4, 8):
+        l = whole[first:first + T]
+        for b in (None, bias[1]):
+            ids, w = check_gate(l, topk, b, n_group=n_group, topk_group=(n_group + 1) // 2, **kw)
+            again, _ = dg.moe_gate(l.clone(), topk, b, n_group=n_group, topk_group=(n_group + 1) // 2, **kw)
+            assert torch.equal(ids, again)
+        g = _rand(T, topk, 5).cuda()
+        for score in ("sigmoid", "softmax"):
+            d = dg.moe_gate_backward(l, ids, g, score=score, d_logits=d_whole[first:first + T])
+            assert torch.equal(d, dg.moe_gate_backward(l.clone(), ids, g, score=score))
+        assert (d_whole[:first] == 7).all() and (d_whole[first + T:] == 7).all()
+        d_whole.fill_(7.0)
+
+
 def test_outputs_beyond_the_rows_stay_and_no_tokens_is_nothing():
     ids = torch.full((12, 3), 77, dtype=torch.int32, device="cuda")
     w = torch.full((12, 3), 77.0, device="cuda")
