@@ -395,7 +395,9 @@ __global__ void __launch_bounds__(kInt8Threads<PIPES>, 1)
       const int zd = MODE == MODE_MASKED ? tl.g : 0;
       const size_t row_g = static_cast<size_t>(zd) * p.rows + m;
       const float sa = valid ? __ldg(p.sa + row_g) : 0.0f;
-      // B's scales of the warp's chunks come in while the tile is computed
+      // B's scales of the warp's chunks come in while the tile is computed (once every
+      // lane has read those of the tile before)
+      __syncwarp();
       const float* sb = p.sb + static_cast<size_t>(expert) * p.N;
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
