@@ -19,14 +19,6 @@ __device__ __forceinline__ bool mbar_test_wait_addr(uint32_t bar, uint32_t parit
   return ok != 0;
 }
 
-// cluster_sync without its release: for threads that have published nothing,
-// have fenced what they did, or whose arrivals the other CTA has waited for.
-__device__ __forceinline__ void cluster_sync_relaxed() {
-  asm volatile("barrier.cluster.arrive.relaxed.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
-
 // D(tmem) (+)= A . B^T, int8 x int8 into int32, one K=32 step.
 template <int CG>
 __device__ __forceinline__ void mma_i8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
