@@ -280,7 +280,7 @@ __device__ __forceinline__ Tile tile_of(int t, const GemmArgs& p, const int* pre
     int g = 0;
     while (prefix[g + 1] <= t) ++g;
     const int local = t - prefix[g];
-    const int cnt = static_cast<int>((static_cast<uint32_t>(counts[g]) + TILE_M - 1) / TILE_M);
+    const int cnt = (counts[g] + TILE_M - 1) / TILE_M;
     tl.g = g;
     tl.n_blk = local / cnt;
     tl.m_blk = local - tl.n_blk * cnt;

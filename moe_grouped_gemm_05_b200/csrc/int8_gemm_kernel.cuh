@@ -21,7 +21,7 @@
 // loading its own 128 rows of A and half of B's.  No load is multicast.
 // A K that is no multiple of 128 ends in a block that the TMA fills with zeros.
 //
-// Measured (BF16 out): 4096x7168x2048 45.4 us, 2.65 POPS; 82% of the busiest
+// Measured (BF16 out): 4096x7168x2048 45.6 us, 2.64 POPS; 82% of the busiest
 // SM's cycles are MMAs, the rest set-up, first load, last epilogue and teardown.
 // Contiguous, 8 experts, 32768 rows, 4096x7168: 600 us before the power cap sets
 // in (3.2 POPS), 735 us under it.  Masked, 16 experts of up to 256 rows,
@@ -78,6 +78,25 @@ struct Int8Layout {
   static_assert(BN % 64 == 0 && BN <= 256 && 2 * kAccStride <= kTmemCols, "two accumulators fit in tensor memory");
   static_assert(kOffEpi % 1024 == 0 && kBBytes % 1024 == 0, "swizzle atoms are 1024-byte aligned");
 };
+
+// tile_of; in the masked layout with an expert's tiles counted without leaving int
+// for counts next to 2^31 (FP8 rows of so many do not fit in memory, 16-byte ones do).
+template <int MODE, int TILE_M>
+__device__ __forceinline__ Tile int8_tile_of(int t, const GemmArgs& p, const int* prefix, const int* counts) {
+  if constexpr (MODE != MODE_MASKED) {
+    return tile_of<MODE, TILE_M>(t, p, prefix, counts);
+  } else {
+    Tile tl;
+    tl.g = 0;
+    while (prefix[tl.g + 1] <= t) ++tl.g;
+    const int local = t - prefix[tl.g];
+    const int blocks = static_cast<int>((static_cast<uint32_t>(counts[tl.g]) + TILE_M - 1) / TILE_M);
+    tl.n_blk = local / blocks;
+    tl.m_blk = local - tl.n_blk * blocks;
+    tl.row0 = tl.m_blk * TILE_M;
+    return tl;
+  }
+}
 
 // One warp: the masked layout's valid rows per expert and running sum of tiles.
 template <int TILE_M>
@@ -225,7 +244,7 @@ __global__ void __launch_bounds__(kInt8Threads<PIPES>, 1)
     const uint32_t full0 = kPair ? mapa_shared(smem_u32(full_bar), 0) : smem_u32(full_bar);
     bool ok = true;
     for (int t = unit0; t < ntiles && ok; t += units) {
-      const Tile tl = tile_of<MODE, L::kTileM>(t, p, prefix, counts);
+      const Tile tl = int8_tile_of<MODE, L::kTileM>(t, p, prefix, counts);
       int grp_a = 0, grp_b = 0;
       if (MODE == MODE_CONTIG) {
         grp_b = contig_expert<CTAS>(tl, p);
@@ -285,7 +304,7 @@ __global__ void __launch_bounds__(kInt8Threads<PIPES>, 1)
       for (int t = unit0; t < ntiles && ok; t += units) {
         int mma_n = BN;
         if (MODE == MODE_CONTIG || ragged_n) {
-          const Tile tl = tile_of<MODE, L::kTileM>(t, p, prefix, counts);
+          const Tile tl = int8_tile_of<MODE, L::kTileM>(t, p, prefix, counts);
           if (MODE == MODE_CONTIG && contig_expert<CTAS>(tl, p) < 0) continue;
           mma_n = tile_mma_n<BN, CTAS, 0>(tl.n_blk * BN, p.N);
         }
@@ -354,7 +373,7 @@ __global__ void __launch_bounds__(kInt8Threads<PIPES>, 1)
     constexpr int kMine = L::kMine;
     uint32_t own = 0;
     for (int t = unit0; t < ntiles; t += units) {
-      const Tile tl = tile_of<MODE, L::kTileM>(t, p, prefix, counts);
+      const Tile tl = int8_tile_of<MODE, L::kTileM>(t, p, prefix, counts);
       int expert = 0, own_e = 0;
       if (MODE == MODE_CONTIG) {
         const int own_blk = tl.row0 / 128 + static_cast<int>(rank);  // a pair's blocks may differ in expert
