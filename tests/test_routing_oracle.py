@@ -66,6 +66,20 @@ def test_quantize_hand_worked():
     assert s[0] == 1 and s[1] == 1 and np.isnan(s[2]) and s[3] == np.float32(2.0 ** -126)
 
 
+def test_codes_are_within_half_a_step():
+    """x is within scale / 2 of code * scale: the scale and the inverse are off by half a
+    step (2^-24) each, which on 127 codes is 127 * 2.01 * 2^-24 of a scale more."""
+    rng = np.random.default_rng(4)
+    x = rng.standard_normal((200, 64)) * np.exp(rng.uniform(-85, 80, (200, 1)))
+    x[:20] = rng.integers(-3, 4, (20, 64)) * 2.0 ** -140          # below the smallest scale
+    x[20:40] = rng.integers(-254, 255, (20, 64)) / 2              # halves: ties
+    x = x.astype(np.float32)
+    q, s = routing.quantize_int8_per_token(x)
+    off = np.abs(x.astype(np.float64) - q * s.astype(np.float64)[:, None])
+    assert (off <= (0.5 + 256 * 2.0 ** -24) * s[:, None]).all()
+    assert (np.abs(q).max(axis=1)[40:] == 127).all() and np.isfinite(s).all()
+
+
 def test_int8_gemm_hand_worked():
     d = routing.int8_gemm(np.array([[1, -2], [-128, 127]], np.int8), np.array([0.5, 2.0], np.float32),
                           np.array([[3, 4], [-128, -128]], np.int8), np.array([1.0, 0.25], np.float32))
