@@ -669,7 +669,8 @@ static const Config* int8_config_table(int* count) {
 
 // Time of one 128-wide K block of a tile and of the rest of a tile, in ns, as
 // in the FP8 kernels' cost model: fitted to 4096x7168x2048 and to contiguous 8 x
-// (512 rows x 4096 x 7168), back to back.
+// (512 rows x 4096 x 7168), back to back, and to no other shape (the calibration
+// module times the FP8 tiles only).
 static const CostParams kCostInt8[] = {
     {64, 1, 1, false, 265, 600},  {128, 1, 1, false, 290, 700},   {256, 1, 1, false, 430, 700},
     {128, 2, 1, false, 285, 750}, {256, 2, 1, false, 385, 800}, {64, 1, 2, true, 385, 900},
@@ -867,6 +868,11 @@ static cudaError_t launch_gate_v(GateArgs& p, cudaStream_t st) {
   // whole runs; with groups, lane tl's is the tl-th of the row only where every group fills its lanes
   p.vec = p.span_log2 >= 0 ? p.gsize == span * V : p.E % V == 0;
   p.full = p.vec && p.E == L * V;
+  // Dealt out where the kept groups have fewer than two lanes a slot.  16384 tokens, dealt
+  // out / left where they are: 256 experts in 8 groups, topk 8, with 2 kept 16.5 / 22.0 us,
+  // 3 kept 17.7 / 17.0, 4 kept 17.9 / 16.3; 512 in 16 groups, topk 8, 4 kept 30.4 / 41.8,
+  // 7 kept 36.5 / 25.2; 1024 in 32 groups, topk 16, 16 kept 101 / 159, 31 kept 131 / 72
+  // (so the border lies nearer to one and a half lanes a slot for the larger rows).
   p.deal = p.span_log2 >= 0 && p.topk_group * span < 2 * p.topk;
   constexpr int th = 32 * kGateWarps, per = th / L;
   const long long blocks = (static_cast<long long>(p.T) + per - 1) / per;

@@ -417,12 +417,14 @@ __device__ __noinline__ int gate_choose64(const GateArgs& p, const LT* row, int 
 // lane counts the ones before its own.  That takes the place of topk rounds of
 // finding and removing the best (which serve the rows with more than 32).
 //
-// Measured, 16384 tokens: 256 experts in 8 groups, topk 8, 16.3 us (topk rounds
-// 37.9); without groups 13.4, without bias 11.6; 64 experts, softmax, topk 6,
-// 6.2 us (a whole warp a token 9.4); 160 experts in 8 groups, 3 kept, 18.8 us (47.6
-// before groups of any size had lanes of their own and few kept experts were dealt
-// out).  Bound by issue, some 710 instructions a token of 256 experts; more resident
-// warps or larger blocks change nothing.
+// Measured, 16384 tokens: 256 experts in 8 groups, topk 8, 16.2 us (topk rounds
+// 37.9), the same with a whole group or all but one of its experts pushed out by a
+// bias of -1e9 or the type's lowest value, 18.9 us with a group masked; without groups
+// 13.4, without bias 11.6; 64 experts, softmax, topk 6, 6.2 us (a whole warp a token
+// 9.4); 160 experts in 8 groups, 3 kept, 18.8 us (47.6 before groups of any size had
+// lanes of their own and few kept experts were dealt out).  Bound by issue, some 740
+// instructions a token of 256 experts in groups; more resident warps or larger blocks
+// change nothing.
 __device__ __forceinline__ float gate_near(float e0, float k) {
   return 2.0f * e0 + fminf(0x1.001p-23f * (1.0f + fabsf(k)), 3.0f);
 }
